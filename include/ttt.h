@@ -323,6 +323,123 @@ ttt_status inplace_ttt_bwd(int T, int d_ff, int d_model, int C, float lr, const 
                            const float* dW_final, void* dZ, void* dVhat, float* dW,
                            void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The operators around the layer: a block of a model reads its hidden states through a norm,
+ * projects them with linear layers (to q, k, v and beta, or to the gate and input of a
+ * recurrence, or to Z of the In-Place layer), mixes them over time and projects the result back
+ * onto the residual stream. No buffer of one call may overlap another one of that call except
+ * where an entry point says so. */
+
+/* Layer norm over rows of d features, with one weight group per head. H = 1 is the ordinary
+ * layer norm of [B, T, d] hidden states; H > 1 with token_major = 1 is the output norm of a TTT
+ * layer: O [B, H, T, d] in, rows of all heads of a token side by side out. */
+typedef struct {
+  int B, H, T;      /* rows: B * H * T < 2^31                                            */
+  int d;            /* features of a row, 1..16384                                       */
+  int dtype;        /* ttt_dtype of X, residual, S, Y, dY, dS, dX                        */
+  int token_major;  /* 0: Y and dY are [B, H, T, d]; 1: [B, T, H, d]                     */
+  float eps;        /* > 0, added to the variance                                        */
+} ttt_norm_config;
+
+/* Forward: s = X + residual (or X),  mean and variance over the row's d features,
+ *     rstd = 1 / sqrt(var + eps),  Y = (s - mean) * rstd * weight + bias.
+ *  in : X [B, H, T, d]; residual (nullable) like X; weight, bias [H, d] float32 (nullable: 1, 0)
+ *  out: Y; S (nullable; only with residual) = s rounded to dtype, the residual stream; mean,
+ *       rstd [B, H, T] float32 (nullable), what the backward reads.
+ * Sums and statistics are float32; Y comes from the unrounded s. S may be X or residual. */
+ttt_status ttt_norm_fwd(const ttt_norm_config* cfg, const void* X, const void* residual,
+                        const float* weight, const float* bias, void* Y, void* S, float* mean,
+                        float* rstd, void* stream);
+
+/* Workspace bytes of ttt_norm_bwd; (size_t)-1 for an invalid or unsupported config. */
+size_t ttt_norm_bwd_workspace_bytes(const ttt_norm_config* cfg);
+
+/* Backward for J = <dY, Y> + <dS, S>: with xh = (S - mean) rstd and g = dY * weight,
+ *     dX = rstd (g - mean_d(g) - xh mean_d(g xh)) + dS,
+ *     dweight = sum over the head's rows of dY xh,  dbias = sum over them of dY.
+ *  in : S [B, H, T, d] (the forward's S; its X without a residual); weight (nullable); mean,
+ *       rstd of the forward; dY; dS (nullable = 0), the gradient that reaches s past the norm
+ *  out: dX [B, H, T, d], the gradient of X and of residual alike (may be dS); dweight, dbias
+ *       [H, d] float32 (each nullable; plain stores, summed in a fixed order). The workspace is
+ *       needed only with dweight or dbias. */
+ttt_status ttt_norm_bwd(const ttt_norm_config* cfg, const void* S, const float* weight,
+                        const float* mean, const float* rstd, const void* dY, const void* dS,
+                        void* dX, float* dweight, float* dbias, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Gated linear recurrence, one decay per feature and token:
+ *     h_t = a_t * h_{t-1} + u_t      (h_{-1} = h0; elementwise over D features)
+ * TTT_GATE_DECAY:   G holds the decay itself (a = G, u = X), float32 as the layer's gamma.
+ * TTT_GATE_SIGMOID: G holds gate logits in dtype (a = sigmoid(G), u = (1 - a) X).
+ * reset (nullable) marks the first token of every document of a packed sequence: at a token with
+ * a nonzero byte the state before it counts as 0, whatever it held. */
+typedef enum { TTT_GATE_DECAY = 0, TTT_GATE_SIGMOID = 1 } ttt_gate;
+typedef struct {
+  int B, T, D;      /* sequences, tokens, features; B * T < 2^31                          */
+  int dtype;        /* ttt_dtype of X, H, dH, dX (and of G, dG with TTT_GATE_SIGMOID)     */
+  int gate;         /* ttt_gate                                                          */
+} ttt_recur_config;
+
+/* Forward. in: X, G [B, T, D]; reset [B, T] bytes (nullable); h0 [B, D] float32 (nullable = 0)
+ * out: H [B, T, D] (every h_t); h_final [B, D] float32 (nullable) = h of the last token. The
+ * state is float32 throughout; H is rounded once. h_final may be h0. */
+ttt_status ttt_recur_fwd(const ttt_recur_config* cfg, const void* X, const void* G,
+                         const unsigned char* reset, const float* h0, void* H, float* h_final,
+                         void* stream);
+
+/* Backward for J = <dH, H> + <dh_final, h_final>: with D_t the adjoint of h_t,
+ *     D_t = dH_t + a_{t+1} D_{t+1}   (+ dh_final on the last token; no term across a reset),
+ *     decay:    dX = D,           dG = D h_{t-1}
+ *     sigmoid:  dX = (1 - a) D,   dG = D (h_{t-1} - X) a (1 - a)
+ *     dh0 = a_0 D_0               (h_{t-1} = 0 at a reset, and dh0 = 0 where token 0 is one).
+ *  in : X (read with TTT_GATE_SIGMOID only, else nullable), G, reset, h0 as in the forward; H
+ *       the forward's output; dH [B, T, D]; dh_final [B, D] float32 (nullable = 0)
+ *  out: dX, dG [B, T, D] in the types of X and G; dh0 [B, D] float32 (nullable; may be
+ *       dh_final). */
+ttt_status ttt_recur_bwd(const ttt_recur_config* cfg, const void* X, const void* G,
+                         const unsigned char* reset, const float* h0, const void* H,
+                         const void* dH, const float* dh_final, void* dX, void* dG, float* dh0,
+                         void* stream);
+
+/* One token of B rows against a cache of states (serving; cfg->T must be 1).
+ *  X, G, Y [B, D]; state [n_slots, D] float32, in and out; slots [B] int32 (device, nullable):
+ *  row b updates state[slots[b]] and Y[b] is the new state. A negative slot marks a padding row:
+ *  its Y row and every state stay as they were. Rows that name the same slot are applied in row
+ *  order, each reading what the one before it left. A slot >= n_slots is skipped like padding
+ *  and recorded as TTT_ERR_RANGE in the device error word. Without slots row b has slot b
+ *  (n_slots >= B). */
+ttt_status ttt_recur_step(const ttt_recur_config* cfg, const void* X, const void* G,
+                          const int* slots, int n_slots, float* state, void* Y, void* stream);
+
+/* Linear layer with a fused epilogue:
+ *     P = X W^T + bias,   Y = act(P) * mul + residual.
+ *  X [M, K], W [N, K], mul, residual (nullable: 1, 0), Y, P [M, N] bf16; bias [N] float32
+ *  (nullable). act is a ttt_act. P (nullable) is written for the backward, rounded to bf16; Y
+ *  comes from the unrounded float32 P and is rounded once. residual may be Y (the residual
+ *  stream updated in place), and so may mul.
+ *  With act = SiLU and mul = H W_up^T this is the gated-MLP activation Z of inplace_ttt_fwd.
+ *  Requirements: N % 8 == 0, K % 8 == 0 (else TTT_ERR_UNSUPPORTED); any M >= 1. */
+ttt_status ttt_linear_fwd(int M, int N, int K, int act, const void* X, const void* W,
+                          const float* bias, const void* mul, const void* residual, void* Y,
+                          void* P, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ttt_linear_fwd (for_bwd = 0) or ttt_linear_bwd (1), 0 if none; (size_t)-1
+ * for invalid or unsupported sizes. */
+size_t ttt_linear_workspace_bytes(int M, int N, int K, int for_bwd);
+
+/* Backward for J = <dY, Y>: with dP = dY * mul * act'(P) (rounded to bf16 for the products),
+ *     dX = dP W,  dW = dP^T X,  dbias = sum over rows of dP,  dmul = dY * act(P);
+ * the gradient of residual is dY itself.
+ *  in : X, W, mul as in the forward; P the forward's P (required with an activation other than
+ *       the identity, and with mul; else not read); dY [M, N] bf16
+ *  out: dX [M, K], dW [N, K], dmul [M, N] bf16, dbias [N] float32, each nullable (at least one
+ *       given; dmul only with mul); plain stores, sums in a fixed order. X is read for dW only
+ *       and W for dX only (each nullable otherwise). */
+ttt_status ttt_linear_bwd(int M, int N, int K, int act, const void* X, const void* W,
+                          const void* P, const void* mul, const void* dY, void* dX, void* dW,
+                          float* dbias, void* dmul, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
 /* Synchronises `stream`, then returns TTT_ERR_TIMEOUT if any kernel of this library on the
  * current device recorded a bounded wait that ran out since the last call, else TTT_ERR_RANGE
  * if one recorded an input outside its range (and clears the word), TTT_ERR_CUDA if the stream

@@ -27,6 +27,7 @@ F32, BF16 = 0, 1
 LOSS = {"mse": 0, "ip": 1}
 ACT = {"id": 0, "silu": 1}
 DECAY = {"scalar": 0, "vector": 1}
+GATE = {"decay": 0, "sigmoid": 1}
 
 
 class TTTError(RuntimeError):
@@ -43,8 +44,20 @@ class ttt_config(ctypes.Structure):
                 ("w0_shared", ctypes.c_int)]
 
 
+class ttt_norm_config(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("token_major", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
+class ttt_recur_config(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("gate", ctypes.c_int)]
+
+
 _p, _i, _u, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
 _cfgp = ctypes.POINTER(ttt_config)
+_normp, _recurp = ctypes.POINTER(ttt_norm_config), ctypes.POINTER(ttt_recur_config)
 _SIGS = {
     "ttt_workspace_bytes": ([_cfgp, _i], _sz),
     "ttt_saved_bytes": ([_cfgp], _sz),
@@ -65,6 +78,15 @@ _SIGS = {
     "inplace_ttt_target": ([_i] * 3 + [_p] * 5 + [_sz, _p], _i),
     "inplace_ttt_target_bwd_workspace_bytes": ([_i] * 3, _sz),
     "inplace_ttt_target_bwd": ([_i] * 3 + [_p] * 8 + [_sz, _p], _i),
+    "ttt_norm_fwd": ([_normp] + [_p] * 9, _i),
+    "ttt_norm_bwd_workspace_bytes": ([_normp], _sz),
+    "ttt_norm_bwd": ([_normp] + [_p] * 10 + [_sz, _p], _i),
+    "ttt_recur_fwd": ([_recurp] + [_p] * 7, _i),
+    "ttt_recur_bwd": ([_recurp] + [_p] * 11, _i),
+    "ttt_recur_step": ([_recurp] + [_p] * 3 + [_i] + [_p] * 3, _i),
+    "ttt_linear_workspace_bytes": ([_i] * 4, _sz),
+    "ttt_linear_fwd": ([_i] * 4 + [_p] * 8 + [_sz, _p], _i),
+    "ttt_linear_bwd": ([_i] * 4 + [_p] * 10 + [_sz, _p], _i),
     "ttt_get_device_error": ([_p], _i),
     "ttt_selftest_bounded_wait": ([_u, _p], _i),
     "ttt_status_string": ([_i], ctypes.c_char_p),
@@ -405,3 +427,168 @@ def inplace_cp_fwd(T, d_ff, d_model, C, lr, Z, Vhat, W, O, workspace, workspace_
     for h in range(rank):
         ops.add(W, parts[h])
     ops.fwd(T, d_ff, d_model, C, lr, Z, Vhat, W, O, workspace, workspace_bytes)
+
+
+def _tensors(where, *specs):
+    """Device addresses of the tensor arguments (name, tensor, elements, dtype) of one call.
+
+    Like _ptr, and each tensor must have the dtype and the number of elements that the call's
+    sizes give it: the C ABI sees addresses only, and a short buffer would be read or written
+    past its end. None and raw integer addresses pass through unchecked."""
+    import torch
+    dev, out = None, []
+    for name, t, n, dtype in specs:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if t.dtype is not dtype or t.numel() != n:
+            raise ValueError(f"{where}: {name} is {t.numel()} x {t.dtype}, expected {n} x {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous (dense row-major)")
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be a CUDA tensor")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, but the library runs on the "
+                             f"current device cuda:{dev}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _dtypes(code):
+    import torch
+    return (torch.bfloat16 if code == BF16 else torch.float32), torch.float32
+
+
+def make_norm_config(B, H, T, d, dtype="bf16", token_major=False, eps=1e-5) -> ttt_norm_config:
+    """Rows of d features, B * H * T of them, with one weight row per head (H = 1: the plain
+    layer norm). token_major: Y and dY are [B, T, H, d] instead of [B, H, T, d]."""
+    return ttt_norm_config(B, H, T, d, F32 if dtype in ("f32", F32) else BF16,
+                           int(bool(token_major)), float(eps))
+
+
+def ttt_norm_fwd(cfg, X, residual, weight, bias, Y, S=None, mean=None, rstd=None, stream=None):
+    """Layer norm forward: s = X + residual (X when residual is None), Y = norm(s) * weight +
+    bias, S = s. X, residual, S [B,H,T,d] and Y ([B,T,H,d] if cfg.token_major) in cfg's dtype;
+    weight, bias [H,d] and mean, rstd [B,H,T] float32. residual, weight, bias, S, mean and rstd
+    may be None."""
+    dt, f32 = _dtypes(cfg.dtype)
+    rows, hd = cfg.B * cfg.H * cfg.T, cfg.H * cfg.d
+    n = rows * cfg.d
+    p = _tensors("ttt_norm_fwd", ("X", X, n, dt), ("residual", residual, n, dt),
+                 ("weight", weight, hd, f32), ("bias", bias, hd, f32), ("Y", Y, n, dt),
+                 ("S", S, n, dt), ("mean", mean, rows, f32), ("rstd", rstd, rows, f32))
+    _check(_lib.ttt_norm_fwd(ctypes.byref(cfg), *p, _stream(stream)), "ttt_norm_fwd")
+
+
+def ttt_norm_bwd_workspace_bytes(cfg) -> int:
+    n = _lib.ttt_norm_bwd_workspace_bytes(ctypes.byref(cfg))
+    if n == ctypes.c_size_t(-1).value:
+        raise TTTError(ERR_INVALID_ARG, "ttt_norm_bwd_workspace_bytes")
+    return n
+
+
+def ttt_norm_bwd(cfg, S, weight, mean, rstd, dY, dS, dX, dweight=None, dbias=None, workspace=None,
+                 workspace_bytes=0, stream=None):
+    """Layer norm backward for J = <dY, Y> + <dS, S> (dS may be None): dX (the gradient of X and
+    of residual), dweight and dbias [H,d] float32 (each may be None). S is the forward's S, or
+    its X without a residual. Workspace: ttt_norm_bwd_workspace_bytes(cfg)."""
+    dt, f32 = _dtypes(cfg.dtype)
+    rows, hd = cfg.B * cfg.H * cfg.T, cfg.H * cfg.d
+    n = rows * cfg.d
+    p = _tensors("ttt_norm_bwd", ("S", S, n, dt), ("weight", weight, hd, f32),
+                 ("mean", mean, rows, f32), ("rstd", rstd, rows, f32), ("dY", dY, n, dt),
+                 ("dS", dS, n, dt), ("dX", dX, n, dt), ("dweight", dweight, hd, f32),
+                 ("dbias", dbias, hd, f32))
+    _check(_lib.ttt_norm_bwd(ctypes.byref(cfg), *p, _ws(workspace, workspace_bytes),
+                             int(workspace_bytes), _stream(stream)), "ttt_norm_bwd")
+
+
+def _ws(t, nbytes):
+    """Address of a workspace tensor that must hold the bytes the caller says it does."""
+    _check_size(t, nbytes, "workspace")
+    return _ptr(t)
+
+
+def make_recur_config(B, T, D, dtype="bf16", gate="sigmoid") -> ttt_recur_config:
+    """gate: "sigmoid" (G holds logits in dtype, u = (1 - a) X) or "decay" (G holds the decay
+    itself, float32, u = X)."""
+    return ttt_recur_config(B, T, D, F32 if dtype in ("f32", F32) else BF16, GATE.get(gate, gate))
+
+
+def ttt_recur_fwd(cfg, X, G, reset, h0, H, h_final=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + u_t over [B,T,D]. reset [B,T] uint8 (a nonzero
+    byte starts a document: the state before that token counts as 0) and h0 [B,D] float32 may be
+    None; H [B,T,D] holds every h_t, h_final [B,D] float32 (or None) the last."""
+    import torch
+    dt, f32 = _dtypes(cfg.dtype)
+    n, bd = cfg.B * cfg.T * cfg.D, cfg.B * cfg.D
+    p = _tensors("ttt_recur_fwd", ("X", X, n, dt), ("G", G, n, dt if cfg.gate else f32),
+                 ("reset", reset, cfg.B * cfg.T, torch.uint8), ("h0", h0, bd, f32),
+                 ("H", H, n, dt), ("h_final", h_final, bd, f32))
+    _check(_lib.ttt_recur_fwd(ctypes.byref(cfg), *p, _stream(stream)), "ttt_recur_fwd")
+
+
+def ttt_recur_bwd(cfg, X, G, reset, h0, H, dH, dh_final, dX, dG, dh0=None, stream=None):
+    """Backward of ttt_recur_fwd for J = <dH, H> + <dh_final, h_final>, from the forward's inputs
+    and its H: dX, dG [B,T,D] in the types of X and G, dh0 [B,D] float32. reset, h0, dh_final and
+    dh0 may be None, and X with the "decay" gate."""
+    import torch
+    dt, f32 = _dtypes(cfg.dtype)
+    n, bd = cfg.B * cfg.T * cfg.D, cfg.B * cfg.D
+    gt = dt if cfg.gate else f32
+    p = _tensors("ttt_recur_bwd", ("X", X, n, dt), ("G", G, n, gt),
+                 ("reset", reset, cfg.B * cfg.T, torch.uint8), ("h0", h0, bd, f32), ("H", H, n, dt),
+                 ("dH", dH, n, dt), ("dh_final", dh_final, bd, f32), ("dX", dX, n, dt),
+                 ("dG", dG, n, gt), ("dh0", dh0, bd, f32))
+    _check(_lib.ttt_recur_bwd(ctypes.byref(cfg), *p, _stream(stream)), "ttt_recur_bwd")
+
+
+def ttt_recur_step(cfg, X, G, slots, state, Y, stream=None):
+    """One token of cfg.B rows (cfg.T = 1) against the state cache [n_slots, D] float32, updated
+    in place: row b reads and writes state[slots[b]] and Y[b] is the new state. slots [B] int32
+    on the device, negative for a padding row (left untouched); None: row b has slot b."""
+    import torch
+    dt, f32 = _dtypes(cfg.dtype)
+    n_slots = state.shape[0]
+    n = cfg.B * cfg.D
+    p = _tensors("ttt_recur_step", ("X", X, n, dt), ("G", G, n, dt if cfg.gate else f32),
+                 ("slots", slots, cfg.B, torch.int32), ("state", state, n_slots * cfg.D, f32),
+                 ("Y", Y, n, dt))
+    _check(_lib.ttt_recur_step(ctypes.byref(cfg), p[0], p[1], p[2], n_slots, p[3], p[4],
+                               _stream(stream)), "ttt_recur_step")
+
+
+def ttt_linear_workspace_bytes(M, N, K, for_bwd) -> int:
+    n = _lib.ttt_linear_workspace_bytes(M, N, K, int(for_bwd))
+    if n == ctypes.c_size_t(-1).value:
+        raise TTTError(ERR_INVALID_ARG, "ttt_linear_workspace_bytes")
+    return n
+
+
+def ttt_linear_fwd(M, N, K, act, X, W, bias, mul, residual, Y, P=None, workspace=None,
+                   workspace_bytes=0, stream=None):
+    """Y = act(X W^T + bias) * mul + residual with act "id" or "silu". X [M,K], W [N,K] (a torch
+    Linear's weight), mul, residual, Y and P [M,N] bf16, bias [N] float32; bias, mul, residual
+    and P may be None. P receives X W^T + bias, which ttt_linear_bwd reads. N and K are multiples
+    of 8. Workspace: ttt_linear_workspace_bytes(M, N, K, 0)."""
+    bf, f32 = _dtypes(BF16)
+    p = _tensors("ttt_linear_fwd", ("X", X, M * K, bf), ("W", W, N * K, bf), ("bias", bias, N, f32),
+                 ("mul", mul, M * N, bf), ("residual", residual, M * N, bf), ("Y", Y, M * N, bf),
+                 ("P", P, M * N, bf))
+    _check(_lib.ttt_linear_fwd(M, N, K, ACT.get(act, act), *p, _ws(workspace, workspace_bytes),
+                               int(workspace_bytes), _stream(stream)), "ttt_linear_fwd")
+
+
+def ttt_linear_bwd(M, N, K, act, X, W, P, mul, dY, dX=None, dW=None, dbias=None, dmul=None,
+                   workspace=None, workspace_bytes=0, stream=None):
+    """Backward of ttt_linear_fwd for J = <dY, Y>: dX [M,K], dW [N,K], dmul [M,N] bf16 and dbias
+    [N] float32, each written when given (the gradient of residual is dY). P is the forward's P;
+    it may be None for act "id" without mul. Workspace: ttt_linear_workspace_bytes(M, N, K, 1)."""
+    bf, f32 = _dtypes(BF16)
+    p = _tensors("ttt_linear_bwd", ("X", X, M * K, bf), ("W", W, N * K, bf), ("P", P, M * N, bf),
+                 ("mul", mul, M * N, bf), ("dY", dY, M * N, bf), ("dX", dX, M * K, bf),
+                 ("dW", dW, N * K, bf), ("dbias", dbias, N, f32), ("dmul", dmul, M * N, bf))
+    _check(_lib.ttt_linear_bwd(M, N, K, ACT.get(act, act), *p, _ws(workspace, workspace_bytes),
+                               int(workspace_bytes), _stream(stream)), "ttt_linear_bwd")

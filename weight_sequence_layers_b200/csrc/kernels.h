@@ -118,6 +118,57 @@ cudaError_t inplace_bwd_run(int T, int d_ff, int d_model, int C, float lr, const
                             const float* dW_final, void* dZ, void* dVhat, float* dW,
                             const bool* reset, void* ws, unsigned* err, cudaStream_t s);
 
+// Layer norm (ttt_norm.cu).
+struct NormArgs {
+  int B, H, T, d;
+  bool bf16, token_major;
+  float eps;
+  const void *X, *residual, *dY, *dS;
+  const float *weight, *bias;
+  void *Y, *S, *dX;
+  float *mean, *rstd;  // written by the forward, read by the backward
+  float *dweight, *dbias;
+  void* ws;
+};
+bool norm_supported(const NormArgs& a);
+size_t norm_bwd_workspace(const NormArgs& a);
+cudaError_t norm_fwd(const NormArgs& a, cudaStream_t s);
+cudaError_t norm_bwd(const NormArgs& a, cudaStream_t s);
+
+// Gated linear recurrence (ttt_recur.cu).
+struct RecurArgs {
+  int B, T, D;
+  bool bf16, sigmoid;
+  const void *X, *G, *H_in, *dH;
+  const unsigned char* reset;
+  const float *h0, *dh_final;
+  void *H, *dX, *dG;
+  float *h_final, *dh0;
+  const int* slots;  // step
+  int n_slots;
+  float* state;
+  unsigned* err;
+};
+cudaError_t recur_fwd(const RecurArgs& a, cudaStream_t s);
+cudaError_t recur_bwd(const RecurArgs& a, cudaStream_t s);
+cudaError_t recur_step(const RecurArgs& a, cudaStream_t s);
+
+// Linear layer with its epilogue (ttt_linear.cu).
+struct LinearArgs {
+  int M, N, K;
+  bool silu;
+  const void *X, *W, *mul, *residual, *dY, *P_in;
+  const float* bias;
+  void *Y, *P, *dX, *dW, *dmul;
+  float* dbias;
+  void* ws;
+  unsigned* err;
+};
+size_t linear_fwd_workspace(int M, int N, int K);
+size_t linear_bwd_workspace(int M, int N, int K);
+cudaError_t linear_fwd(const LinearArgs& a, cudaStream_t s);
+cudaError_t linear_bwd(const LinearArgs& a, cudaStream_t s);
+
 // Address of the current device's error word (looked up once per device); NULL on failure.
 unsigned* current_error_word();
 

@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/ttt.h"
 #include "kernels.h"
 
@@ -73,6 +75,8 @@ ttt_status ttt_norm_fwd(const ttt_norm_config* cfg, const void* X, const void* r
   if (!aligned16({X, residual, weight, bias, Y, S, mean, rstd})) return TTT_ERR_ALIGNMENT;
   a.X = X; a.residual = residual; a.weight = weight; a.bias = bias; a.Y = Y; a.S = S;
   a.mean = mean; a.rstd = rstd;
+  a.err = current_error_word();
+  if (!a.err) return TTT_ERR_CUDA;
   return status_of(norm_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -96,6 +100,8 @@ ttt_status ttt_norm_bwd(const ttt_norm_config* cfg, const void* S, const float* 
   a.X = S; a.weight = weight; a.mean = const_cast<float*>(mean);
   a.rstd = const_cast<float*>(rstd); a.dY = dY; a.dS = dS; a.dX = dX; a.dweight = dweight;
   a.dbias = dbias; a.ws = workspace;
+  a.err = current_error_word();
+  if (!a.err) return TTT_ERR_CUDA;
   return status_of(norm_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 

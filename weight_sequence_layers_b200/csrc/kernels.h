@@ -129,6 +129,7 @@ struct NormArgs {
   float *mean, *rstd;  // written by the forward, read by the backward
   float *dweight, *dbias;
   void* ws;
+  unsigned* err;
 };
 bool norm_supported(const NormArgs& a);
 size_t norm_bwd_workspace(const NormArgs& a);

@@ -5,8 +5,8 @@
 // mean, then the centred squares: no cancellation for rows with a large mean) and written once.
 // A row belongs to a group of threads: 8 to 32 lanes of a warp for narrow rows (several rows
 // per CTA, sums by shuffles alone), the whole CTA for wide ones. CTA (h, s) walks a contiguous
-// run of the rows of head h, so that the head's weights stay in registers, and loads the next
-// row before it reduces the current one.
+// run of the rows of head h, so that the head's weights stay in registers, with the next rows'
+// loads in flight.
 //
 // The backward keeps its share of dweight and dbias in registers over its run; the CTAs' shares
 // go to the workspace and a second kernel adds them in a fixed order (no atomics). That kernel
@@ -16,6 +16,7 @@
 
 #include <algorithm>
 
+#include "common.cuh"
 #include "kernels.h"
 #include "simt_util.cuh"
 
@@ -26,8 +27,35 @@ using bf16 = __nv_bfloat16;
 constexpr int kSMs = 148;
 constexpr int kNarrowThreads = 128;  // CTA of the narrow-row kernels
 
+// Pairs of float32 in one instruction (add, mul, fma on f32x2): the kernels are bound by the
+// instructions they issue before they are by HBM (a 16-byte access holds eight bf16), and a pair
+// costs one issue slot.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 c;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(c.x), "=f"(c.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return c;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 c;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(c.x), "=f"(c.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return c;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 d) {
+  float2 c;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(c.x), "=f"(c.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(d.x), "f"(d.y));
+  return c;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // VEC elements of a row: one 16-byte access, or one element where the width does not keep rows
-// on 16-byte boundaries. Plain (coherent) loads: S may be X or residual, dX may be dS.
+// on 16-byte boundaries. Coherent loads, since S may be X or residual and dX may be dS.
 template <typename E, int VEC>
 struct Pack;
 template <>
@@ -37,21 +65,16 @@ struct Pack<bf16, 8> {
     asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(float2* v) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
+    for (int k = 0; k < 4; ++k)
+      v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ void store(bf16* p, const float (&v)[8]) {
+  static __device__ __forceinline__ void store(bf16* p, const float2* v) {
     uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
+    for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(v[k].x, v[k].y);
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
@@ -62,171 +85,259 @@ struct Pack<float, 4> {
     asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];"
                  : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p) : "memory");
   }
-  __device__ __forceinline__ void get(float (&v)[4]) const {
-    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+  __device__ __forceinline__ void get(float2* v) const {
+    v[0] = make_float2(r.x, r.y);
+    v[1] = make_float2(r.z, r.w);
   }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  static __device__ __forceinline__ void store(float* p, const float2* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
   }
 };
 template <typename E>
 struct Pack<E, 1> {
   E r;
   __device__ __forceinline__ void load(const E* p) { r = *p; }
-  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = ldf(&r); }
-  static __device__ __forceinline__ void store(E* p, const float (&v)[1]) { stf(p, v[0]); }
 };
 
-template <int VEC>
-__device__ __forceinline__ void load_f32(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = *p;
-  } else {
+// A thread's part of a row: NV accesses of VEC elements, `step` accesses apart, as pairs. VEC = 1
+// has an odd element only with NV = 1 (the pair's second half stays 0). Elements past the
+// row's end read as 0.
+template <typename E, int VEC, int NV>
+struct Frag {
+  static constexpr int NP = VEC == 1 ? (NV + 1) / 2 : NV * VEC / 2;  // pairs
+  int first, step, d;  // this thread's first column and the columns between its accesses
+  __device__ __forceinline__ int col(int n) const { return first + n * step; }
+  __device__ __forceinline__ bool ok(int n) const { return col(n) < d; }
+  // unpacks loaded accesses
+  __device__ __forceinline__ void get(const Pack<E, VEC> (&p)[NV], float2 (&v)[NP]) const {
+    if constexpr (VEC > 1) {
 #pragma unroll
-    for (int k = 0; k < VEC; k += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(p + k);
-      v[k] = f.x; v[k + 1] = f.y; v[k + 2] = f.z; v[k + 3] = f.w;
+      for (int n = 0; n < NV; ++n) {
+        if (ok(n)) p[n].get(v + n * VEC / 2);
+        else
+#pragma unroll
+          for (int k = 0; k < VEC / 2; ++k) v[n * VEC / 2 + k] = both(0.f);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 2 * NP; n += 2)
+        v[n / 2] = make_float2(ok(n) ? ldf(&p[n].r) : 0.f,
+                               n + 1 < NV && ok(n + 1) ? ldf(&p[n + 1 < NV ? n + 1 : 0].r) : 0.f);
     }
   }
+  template <typename L>
+  __device__ __forceinline__ void each_f32(L f) const {  // f(pair, half, column) where valid
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+      if (ok(n))
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f((n * VEC + k) / 2, (n * VEC + k) & 1, col(n) + k);
+  }
+  __device__ __forceinline__ void get_f32(const float* p, float none, float2 (&v)[NP]) const {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) v[k] = both(none);
+    if (!p) return;
+    each_f32([&](int i, int h, int c) { (h ? v[i].y : v[i].x) = p[c]; });
+  }
+  __device__ __forceinline__ void store(E* p, const float2 (&v)[NP]) const {
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+      if (ok(n)) {
+        if constexpr (VEC > 1) Pack<E, VEC>::store(p + col(n), v + n * VEC / 2);
+        else stf(p + col(n), n & 1 ? v[n / 2].y : v[n / 2].x);
+      }
+  }
+  // x - mean with elements past the end kept at 0
+  __device__ __forceinline__ void centre(float mean, float2 (&v)[NP]) const {
+    const float2 m = both(-mean);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if constexpr (VEC > 1) {
+        if (ok(2 * i / VEC)) v[i] = add2(v[i], m);
+      } else {
+        v[i].x = ok(2 * i) ? v[i].x - mean : 0.f;
+        v[i].y = 2 * i + 1 < NV && ok(2 * i + 1) ? v[i].y - mean : 0.f;
+      }
+    }
+  }
+};
+template <int NP>
+__device__ __forceinline__ float total(const float2 (&v)[NP]) {
+  float2 t = v[0];
+#pragma unroll
+  for (int i = 1; i < NP; ++i) t = add2(t, v[i]);
+  return t.x + t.y;
+}
+template <int NP>
+__device__ __forceinline__ float total_sq(const float2 (&v)[NP]) {
+  float2 t = mul2(v[0], v[0]);
+#pragma unroll
+  for (int i = 1; i < NP; ++i) t = fma2(v[i], v[i], t);
+  return t.x + t.y;
+}
+template <int NP>
+__device__ __forceinline__ void scale_shift(float rstd, const float2 (&w)[NP],
+                                            const float2 (&b)[NP], float2 (&v)[NP]) {
+  const float2 r = both(rstd);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], r), w[i], b[i]);
+}
+// The backward of one row in two halves. first: x -> xh, g (dY) -> g w, the weight gradients'
+// terms, and the sums of g w and g w xh; second: g w -> dX without dS.
+template <int NP>
+__device__ __forceinline__ void bwd_first(float mean, float rstd, const float2 (&w)[NP],
+                                          float2 (&x)[NP], float2 (&g)[NP], float2 (&dw)[NP],
+                                          float2 (&db)[NP], float& s1, float& s2) {
+  const float2 r = both(rstd), m = both(-mean);
+  float2 t1 = both(0.f), t2 = both(0.f);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    x[i] = mul2(add2(x[i], m), r);
+    db[i] = add2(db[i], g[i]);
+    dw[i] = fma2(g[i], x[i], dw[i]);
+    g[i] = mul2(g[i], w[i]);
+    t1 = add2(t1, g[i]);
+    t2 = fma2(g[i], x[i], t2);
+  }
+  s1 = t1.x + t1.y;
+  s2 = t2.x + t2.y;
+}
+template <int NP>
+__device__ __forceinline__ void bwd_second(float rstd, float c1, float c2, const float2 (&x)[NP],
+                                           float2 (&g)[NP]) {
+  const float2 r = both(rstd), n1 = both(-c1), n2 = both(-c2);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) g[i] = mul2(r, fma2(x[i], n2, add2(g[i], n1)));
 }
 
-// How a launch cuts the rows: head h's B T rows into S runs of L, CTA h S + s.
+// How a launch cuts the rows: head h's B T rows (i = b T + t) into S runs of L, CTA h S + s.
 struct Split {
   int S, L;
 };
-
-struct Rows {
-  int lo, hi, h, T, H, d;
-  bool token_major;
-  // offset of the head's i-th row in the [B, H, T, d] tensors, and in Y and dY
-  __device__ __forceinline__ size_t row(int i) const {
-    const int b = i / T, t = i - b * T;
-    return ((size_t)b * H + h) * T + t;
+// A walk over a head's rows i, i + step, ...: the row in the [B, H, T, d] tensors without a
+// division per step.
+struct Walk {
+  int i, t;      // the head's row and its token
+  size_t row;    // (b H + h) T + t
+  __device__ __forceinline__ void start(int i0, int T, int H, int h) {
+    i = i0;
+    const int b = i0 / T;
+    t = i0 - b * T;
+    row = ((size_t)b * H + h) * T + t;
   }
-  __device__ __forceinline__ size_t yrow(int i) const {
-    return token_major ? (size_t)i * H + h : row(i);  // i = b T + t
+  __device__ __forceinline__ void next(int step, int T, int H) {
+    i += step;
+    row += step;
+    if (H == 1) return;
+    t += step;
+    while (t >= T) {
+      t -= T;
+      row += (size_t)(H - 1) * T;
+    }
   }
 };
-__device__ __forceinline__ Rows rows_of(const NormArgs& a, const Split& sp) {
-  Rows r;
-  r.h = blockIdx.x / sp.S;
-  const int s = blockIdx.x - r.h * sp.S;
-  r.lo = (int)min((long long)s * sp.L, (long long)a.B * a.T);
-  r.hi = (int)min((long long)r.lo + sp.L, (long long)a.B * a.T);
-  r.T = a.T; r.H = a.H; r.d = a.d;
-  r.token_major = a.token_major;
-  return r;
-}
-
-// Sums v over the row's group: G lanes of a warp, or (G = 0) the CTA through red[buf]. The two
-// buffers alternate, so that one barrier per sum is enough: nobody writes a buffer before all
-// have passed the barrier of the sum after the one that last read it.
-template <int G>
-__device__ __forceinline__ float group_sum(float v, float* red) {
-#pragma unroll
-  for (int o = (G ? G : 32) / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  if constexpr (G == 0) {
-    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < nw ? red[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+struct Rows {
+  int lo, hi, s, h;
+  __device__ __forceinline__ Rows(const NormArgs& a, const Split& sp) {
+    h = blockIdx.x / sp.S;
+    s = blockIdx.x - h * sp.S;
+    const long long bt = (long long)a.B * a.T;
+    lo = (int)min((long long)s * sp.L, bt);
+    hi = (int)min((long long)lo + sp.L, bt);
   }
-  return v;
+};
+// The row of Y and dY.
+__device__ __forceinline__ size_t y_row(const NormArgs& a, const Rows& R, const Walk& w) {
+  return a.token_major ? (size_t)w.i * a.H + R.h : w.row;
 }
 
-// E: storage type; VEC: elements of one access; NV: accesses per thread; G: lanes per row (0:
-// the CTA).
-template <typename E, int VEC, int NV, int G>
-__global__ void __launch_bounds__(G ? kNarrowThreads : 512)
-    norm_fwd_kernel(const __grid_constant__ NormArgs a, const Split sp) {
-  __shared__ float red[2][32];
-  const Rows R = rows_of(a, sp);
-  const int gsz = G ? G : blockDim.x, ngrp = G ? kNarrowThreads / G : 1;
-  const int grp = G ? threadIdx.x / gsz : 0, tid = G ? threadIdx.x % gsz : threadIdx.x;
-  const int d = a.d;
+template <int G, int N>
+__device__ __forceinline__ void lanes_sum(float (&v)[N]) {
+#pragma unroll
+  for (int o = G / 2; o; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(~0u, v[n], o);
+}
+
+// ------------------------------------------------------------------------------ narrow rows
+// G lanes per row, NV accesses of VEC elements each, RU rows per group and step: RU rows are
+// loaded ahead while RU are reduced, which keeps enough bytes in flight. RES: with a residual,
+// which doubles a row's bytes.
+template <typename E, int VEC, int NV, int G, int RU, bool RES>
+__global__ void __launch_bounds__(kNarrowThreads)
+    norm_fwd_narrow(const __grid_constant__ NormArgs a, const Split sp) {
+  using F = Frag<E, VEC, NV>;
+  constexpr int NG = kNarrowThreads / G, STEP = RU * NG;
+  const Rows R(a, sp);
+  const int grp = threadIdx.x / G, tid = threadIdx.x % G, d = a.d;
+  const F f{tid * VEC, G * VEC, d};
   const float inv_d = 1.f / (float)d;
   const E* X = static_cast<const E*>(a.X);
   const E* Rs = static_cast<const E*>(a.residual);
   E* Y = static_cast<E*>(a.Y);
   E* S = static_cast<E*>(a.S);
-  float w[NV][VEC], bb[NV][VEC];
-  bool ok[NV];
-  int col[NV];
-  Pack<E, VEC> px[NV], pr[NV];
+  float2 w[F::NP], bb[F::NP];
+  Pack<E, VEC> px[RU][NV], pr[RES ? RU : 1][NV];
+  Walk at[RU];
+  auto fetch = [&]() {
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    col[n] = (tid + n * gsz) * VEC;
-    ok[n] = col[n] < d;
-  }
-  auto fetch = [&](int i) {
-    if (i >= R.hi) return;
-    const size_t o = R.row(i) * d;
+    for (int u = 0; u < RU; ++u)
+      if (at[u].i < R.hi) {
+        const size_t o = at[u].row * d;
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (ok[n]) {
-        px[n].load(X + o + col[n]);
-        if (Rs) pr[n].load(Rs + o + col[n]);
+        for (int n = 0; n < NV; ++n)
+          if (f.ok(n)) {
+            px[u][n].load(X + o + f.col(n));
+            if constexpr (RES) pr[u][n].load(Rs + o + f.col(n));
+          }
       }
   };
-  fetch(R.lo + grp);
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
+  for (int u = 0; u < RU; ++u) at[u].start(R.lo + u * NG + grp, a.T, a.H, R.h);
+  fetch();
+  f.get_f32(a.weight ? a.weight + (size_t)R.h * d : nullptr, 1.f, w);
+  f.get_f32(a.bias ? a.bias + (size_t)R.h * d : nullptr, 0.f, bb);
+  for (int i0 = R.lo; i0 < R.hi; i0 += STEP) {  // uniform over the CTA
+    float2 v[RU][F::NP];
+    float t[RU], mean[RU];
+    size_t row[RU], yrow[RU];
+    bool live[RU];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) { w[n][k] = 1.f; bb[n][k] = 0.f; }
-    if (ok[n]) {
-      if (a.weight) load_f32<VEC>(a.weight + (size_t)R.h * d + col[n], w[n]);
-      if (a.bias) load_f32<VEC>(a.bias + (size_t)R.h * d + col[n], bb[n]);
-    }
-  }
-  for (int i0 = R.lo; i0 < R.hi; i0 += ngrp) {  // uniform over the CTA
-    const int i = i0 + grp;
-    const bool live = i < R.hi;
-    float v[NV][VEC];
-    float sum = 0.f;
+    for (int u = 0; u < RU; ++u) {
+      live[u] = at[u].i < R.hi;
+      row[u] = at[u].row;
+      yrow[u] = y_row(a, R, at[u]);
+      f.get(px[u], v[u]);
+      if constexpr (RES) {
+        float2 r[F::NP];
+        f.get(pr[u], r);
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) v[n][k] = 0.f;
-      if (live && ok[n]) {
-        px[n].get(v[n]);
-        if (Rs) {
-          float r[VEC];
-          pr[n].get(r);
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) v[n][k] += r[k];
-          if (S) Pack<E, VEC>::store(S + R.row(i) * d + col[n], v[n]);
-        }
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) sum += v[n][k];
+        for (int i = 0; i < F::NP; ++i) v[u][i] = add2(v[u][i], r[i]);
+        if (S && live[u]) f.store(S + row[u] * d, v[u]);
       }
+      t[u] = total(v[u]);
+      at[u].next(STEP, a.T, a.H);
     }
-    fetch(i + ngrp);
-    const float mean = group_sum<G>(sum, red[0]) * inv_d;
-    float sq = 0.f;
+    fetch();
+    lanes_sum<G>(t);
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (ok[n])
+    for (int u = 0; u < RU; ++u) {
+      mean[u] = t[u] * inv_d;
+      f.centre(mean[u], v[u]);
+      t[u] = total_sq(v[u]);
+    }
+    lanes_sum<G>(t);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          v[n][k] -= mean;
-          sq = fmaf(v[n][k], v[n][k], sq);
+    for (int u = 0; u < RU; ++u)
+      if (live[u]) {
+        const float rstd = rsqrtf(fmaf(t[u], inv_d, a.eps));
+        scale_shift(rstd, w, bb, v[u]);
+        f.store(Y + yrow[u] * d, v[u]);
+        if (tid == 0) {
+          if (a.mean) a.mean[row[u]] = mean[u];
+          if (a.rstd) a.rstd[row[u]] = rstd;
         }
-    const float rstd = 1.f / sqrtf(group_sum<G>(sq, red[1]) * inv_d + a.eps);
-    if (!live) continue;
-    E* y = Y + R.yrow(i) * d;
-#pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (ok[n]) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) v[n][k] = fmaf(v[n][k] * rstd, w[n][k], bb[n][k]);
-        Pack<E, VEC>::store(y + col[n], v[n]);
       }
-    if (tid == 0) {
-      if (a.mean) a.mean[R.row(i)] = mean;
-      if (a.rstd) a.rstd[R.row(i)] = rstd;
-    }
   }
 }
 
@@ -237,140 +348,390 @@ struct Partials {
   size_t ldp;
 };
 
-template <typename E, int VEC, int NV, int G>
-__global__ void __launch_bounds__(G ? kNarrowThreads : 512)
-    norm_bwd_kernel(const __grid_constant__ NormArgs a, const Split sp, const Partials pt) {
-  __shared__ float red[2][2][32];
-  __shared__ float join[G ? 2 * kNarrowThreads * NV * VEC : 1];
+template <typename E, int VEC, int NV, int G, int RU>
+__global__ void __launch_bounds__(kNarrowThreads)
+    norm_bwd_narrow(const __grid_constant__ NormArgs a, const Split sp, const Partials pt) {
+  using F = Frag<E, VEC, NV>;
+  constexpr int NG = kNarrowThreads / G, STEP = RU * NG;
+  constexpr int W = G * NV * VEC;  // columns of a group, padded
+  __shared__ float join[2][NG][W];
   asm volatile("griddepcontrol.launch_dependents;");
-  const Rows R = rows_of(a, sp);
-  const int gsz = G ? G : blockDim.x, ngrp = G ? kNarrowThreads / G : 1;
-  const int grp = G ? threadIdx.x / gsz : 0, tid = G ? threadIdx.x % gsz : threadIdx.x;
-  const int d = a.d;
+  const Rows R(a, sp);
+  const int grp = threadIdx.x / G, tid = threadIdx.x % G, d = a.d;
+  const F f{tid * VEC, G * VEC, d};
   const float inv_d = 1.f / (float)d;
   const E* X = static_cast<const E*>(a.X);
   const E* dY = static_cast<const E*>(a.dY);
   const E* dS = static_cast<const E*>(a.dS);
   E* dX = static_cast<E*>(a.dX);
-  float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
-  bool ok[NV];
-  int col[NV];
-  Pack<E, VEC> px[NV], py[NV], ps[NV];
-  float nmean = 0.f, nrstd = 0.f;
+  float2 w[F::NP], dw[F::NP], db[F::NP];
+  Pack<E, VEC> px[RU][NV], py[RU][NV], ps[RU][NV];
+  Walk at[RU];
+  float nmean[RU], nrstd[RU];
+  auto fetch = [&]() {
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    col[n] = (tid + n * gsz) * VEC;
-    ok[n] = col[n] < d;
-  }
-  auto fetch = [&](int i) {
-    if (i >= R.hi) return;
-    const size_t row = R.row(i), o = row * d, oy = R.yrow(i) * d;
-    nmean = a.mean[row];
-    nrstd = a.rstd[row];
+    for (int u = 0; u < RU; ++u) {
+      nmean[u] = nrstd[u] = 0.f;
+      if (at[u].i < R.hi) {
+        const size_t o = at[u].row * d, oy = y_row(a, R, at[u]) * d;
+        nmean[u] = a.mean[at[u].row];
+        nrstd[u] = a.rstd[at[u].row];
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (ok[n]) {
-        px[n].load(X + o + col[n]);
-        py[n].load(dY + oy + col[n]);
-        if (dS) ps[n].load(dS + o + col[n]);
+        for (int n = 0; n < NV; ++n)
+          if (f.ok(n)) {
+            px[u][n].load(X + o + f.col(n));
+            py[u][n].load(dY + oy + f.col(n));
+            if (dS) ps[u][n].load(dS + o + f.col(n));
+          }
       }
+    }
   };
-  fetch(R.lo + grp);
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
+  for (int u = 0; u < RU; ++u) at[u].start(R.lo + u * NG + grp, a.T, a.H, R.h);
+  fetch();
+  f.get_f32(a.weight ? a.weight + (size_t)R.h * d : nullptr, 1.f, w);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) { w[n][k] = 1.f; dw[n][k] = db[n][k] = 0.f; }
-    if (ok[n] && a.weight) load_f32<VEC>(a.weight + (size_t)R.h * d + col[n], w[n]);
-  }
-  int it = 0;
-  for (int i0 = R.lo; i0 < R.hi; i0 += ngrp, ++it) {  // uniform over the CTA
-    const int i = i0 + grp;
-    const bool live = i < R.hi;
-    const float mean = nmean, rstd = nrstd;
-    float xh[NV][VEC], g[NV][VEC], s[NV][VEC];
-    float s1 = 0.f, s2 = 0.f;
+  for (int i = 0; i < F::NP; ++i) dw[i] = db[i] = both(0.f);
+  for (int i0 = R.lo; i0 < R.hi; i0 += STEP) {  // uniform over the CTA
+    float2 xh[RU][F::NP], g[RU][F::NP];
+    Pack<E, VEC> s[RU][NV];
+    float t[2 * RU], rstd[RU];
+    size_t row[RU];
+    bool live[RU];
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (live && ok[n]) {
-        px[n].get(xh[n]);
-        py[n].get(g[n]);
-        if (dS) ps[n].get(s[n]);
+    for (int u = 0; u < RU; ++u) {
+      live[u] = at[u].i < R.hi;
+      row[u] = at[u].row;
+      rstd[u] = nrstd[u];
+      t[2 * u] = t[2 * u + 1] = 0.f;
+      if (live[u]) {
+        f.get(px[u], xh[u]);
+        f.get(py[u], g[u]);
+        bwd_first(nmean[u], rstd[u], w, xh[u], g[u], dw, db, t[2 * u], t[2 * u + 1]);
+        if (dS)
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          xh[n][k] = (xh[n][k] - mean) * rstd;
-          db[n][k] += g[n][k];
-          dw[n][k] = fmaf(g[n][k], xh[n][k], dw[n][k]);
-          g[n][k] *= w[n][k];
-          s1 += g[n][k];
-          s2 = fmaf(g[n][k], xh[n][k], s2);
-        }
+          for (int n = 0; n < NV; ++n) s[u][n] = ps[u][n];
       }
-    fetch(i + ngrp);
-#pragma unroll
-    for (int o = (G ? G : 32) / 2; o; o >>= 1) {
-      s1 += __shfl_xor_sync(~0u, s1, o);
-      s2 += __shfl_xor_sync(~0u, s2, o);
+      at[u].next(STEP, a.T, a.H);
     }
-    if constexpr (G == 0) {  // both sums behind one barrier
-      const int nw = blockDim.x >> 5, lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-      if (lane == 0) { red[it & 1][0][wp] = s1; red[it & 1][1][wp] = s2; }
-      __syncthreads();
-      s1 = lane < nw ? red[it & 1][0][lane] : 0.f;
-      s2 = lane < nw ? red[it & 1][1][lane] : 0.f;
+    fetch();
+    lanes_sum<G>(t);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        s1 += __shfl_xor_sync(~0u, s1, o);
-        s2 += __shfl_xor_sync(~0u, s2, o);
-      }
-    }
-    if (!live) continue;
-    const float c1 = s1 * inv_d, c2 = s2 * inv_d;
-    E* dx = dX + R.row(i) * d;
+    for (int u = 0; u < RU; ++u)
+      if (live[u]) {
+        bwd_second(rstd[u], t[2 * u] * inv_d, t[2 * u + 1] * inv_d, xh[u], g[u]);
+        if (dS) {
+          float2 sv[F::NP];
+          f.get(s[u], sv);
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (ok[n]) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float v = rstd * (g[n][k] - c1 - xh[n][k] * c2);
-          g[n][k] = dS ? v + s[n][k] : v;
+          for (int i = 0; i < F::NP; ++i) g[u][i] = add2(g[u][i], sv[i]);
         }
-        Pack<E, VEC>::store(dx + col[n], g[n]);
+        f.store(dX + row[u] * d, g[u]);
       }
   }
   if (!pt.dw0 && !pt.db0) return;
-  const size_t base = (size_t)(blockIdx.x - R.h * sp.S) * pt.ldp + (size_t)R.h * d;
-  if constexpr (G == 0) {
+  // past the row's end the columns hold zeros or, for VEC = 1 pairs, nothing is written
+  f.each_f32([&](int i, int h, int c) {
+    join[0][grp][c] = h ? dw[i].y : dw[i].x;
+    join[1][grp][c] = h ? db[i].y : db[i].x;
+  });
+  __syncthreads();
+  const size_t base = R.s * pt.ldp + (size_t)R.h * d;
+  for (int j = threadIdx.x; j < d; j += kNarrowThreads) {
+    float tw = 0.f, tb = 0.f;
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (ok[n]) {
-        if (pt.dw0)
+    for (int g = 0; g < NG; ++g) {
+      tw += join[0][g][j];
+      tb += join[1][g][j];
+    }
+    if (pt.dw0) pt.dw0[base + j] = tw;
+    if (pt.db0) pt.db0[base + j] = tb;
+  }
+}
+
+// -------------------------------------------------------------------------------- wide rows
+// One CTA per row. Rows come into a ring of shared-memory stages by bulk copies (TMA, untiled)
+// that one thread issues several rows ahead, so that the bytes in flight cost no registers.
+// A stage is refilled behind the barrier of its row's sum, when all threads hold the row in
+// registers. A bulk copy moves whole 16-byte blocks: where rows start off such a boundary
+// (VEC = 1) the stage holds the blocks around the row and the row starts `off` bytes in; the
+// copy never goes past the tensor's last whole block, and the elements behind it (of the last
+// row only) are read directly.
+struct Ring {
+  int stages;
+  uint32_t slot;  // bytes of one row's slot, a multiple of 16
+};
+struct RowView {
+  uint32_t off;  // bytes from the slot's start to the row
+  int in_slot;   // elements of the row that the slot holds
+};
+template <typename E, int VEC>
+__device__ __forceinline__ RowView row_view(size_t row, int d, size_t total_rows) {
+  if (VEC > 1) return {0u, d};
+  const size_t b0 = row * d * sizeof(E), end = total_rows * d * sizeof(E) & ~(size_t)15;
+  const size_t held = end > b0 ? (end - b0) / sizeof(E) : 0;
+  return {(uint32_t)(b0 & 15), held < (size_t)d ? (int)held : d};
+}
+// Bytes that the copy of a row moves.
+template <typename E, int VEC>
+__device__ __forceinline__ uint32_t row_bytes(size_t row, int d, size_t total_rows) {
+  const size_t es = sizeof(E), b0 = row * d * es;
+  if (VEC > 1) return (uint32_t)(d * es);
+  const size_t from = b0 & ~(size_t)15, end = total_rows * d * es & ~(size_t)15;
+  const size_t to = (b0 + d * es + 15) & ~(size_t)15;
+  const size_t stop = to < end ? to : end;
+  return stop > from ? (uint32_t)(stop - from) : 0u;
+}
+template <typename E>
+__device__ __forceinline__ void row_copy(uint32_t slot, const E* base, size_t row, int d,
+                                         uint32_t bytes, uint32_t bar) {
+  if (!bytes) return;
+  const char* src =
+      reinterpret_cast<const char*>(base) + (row * d * sizeof(E) & ~(size_t)15);
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(slot), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+template <typename E, int VEC, int NV>
+__device__ __forceinline__ void slot_read(const Frag<E, VEC, NV>& f, const uint8_t* slot,
+                                          const RowView& rv, const E* row,
+                                          float2 (&v)[Frag<E, VEC, NV>::NP]) {
+  Pack<E, VEC> p[NV];
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) pt.dw0[base + col[n] + k] = dw[n][k];
-        if (pt.db0)
+  for (int n = 0; n < NV; ++n)
+    if (f.ok(n)) {
+      const E* sp = reinterpret_cast<const E*>(slot + rv.off) + f.col(n);
+      if constexpr (VEC == 1) p[n].r = f.col(n) < rv.in_slot ? *sp : row[f.col(n)];
+      else p[n].r = *reinterpret_cast<const decltype(p[n].r)*>(sp);
+    }
+  f.get(p, v);
+}
+
+constexpr int kMaxStages = 8;
+struct __align__(16) RingBars {
+  float red[2][4][16];  // [buffer][value][warp]
+  uint64_t full[kMaxStages];
+  int abort_flag;
+};
+// Sums of N values over the CTA (at most 16 warps) through one barrier. Two buffers alternate:
+// nobody writes a buffer before all have passed the barrier of the sum after the one that last
+// read it.
+template <int N>
+__device__ __forceinline__ void cta_sum(float (&v)[N], float (*red)[16]) {
+  lanes_sum<32>(v);
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  if (lane == 0)
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) pt.db0[base + col[n] + k] = db[n][k];
-      }
-  } else {
-    constexpr int W = G * NV * VEC;  // columns of a group, padded
+    for (int n = 0; n < N; ++n) red[n][wp] = v[n];
+  __syncthreads();
+  const int nw = blockDim.x >> 5;
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
+  for (int n = 0; n < N; ++n) {
+    float t = 0.f;
+    for (int k = 0; k < nw; k += 4) {  // the unused warps' entries are zero
+      const float4 q = *reinterpret_cast<const float4*>(&red[n][k]);
+      t += (q.x + q.y) + (q.z + q.w);
+    }
+    v[n] = t;
+  }
+}
+__device__ __forceinline__ void ring_init(RingBars& bars, const Ring& rg) {
+  for (int k = threadIdx.x; k < 2 * 4 * 16; k += blockDim.x) (&bars.red[0][0][0])[k] = 0.f;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < rg.stages; ++s) mbar_init(smem_u32(&bars.full[s]), 1);
+    bars.abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+}
+
+template <typename E, int VEC, int NV>
+__global__ void __launch_bounds__(512)
+    norm_fwd_wide(const __grid_constant__ NormArgs a, const Split sp, const Ring rg) {
+  using F = Frag<E, VEC, NV>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ RingBars bars;
+  const Rows R(a, sp);
+  const int tid = threadIdx.x, d = a.d;
+  const F f{tid * VEC, (int)blockDim.x * VEC, d};
+  const float inv_d = 1.f / (float)d;
+  const size_t total_rows = (size_t)a.B * a.H * a.T;
+  const E* X = static_cast<const E*>(a.X);
+  const E* Rs = static_cast<const E*>(a.residual);
+  E* Y = static_cast<E*>(a.Y);
+  E* S = static_cast<E*>(a.S);
+  const Abort ab{&bars.abort_flag, a.err};
+  const int nsrc = Rs ? 2 : 1;
+  ring_init(bars, rg);
+  Walk ahead, at;  // the row to load next (one thread) and the row at hand
+  ahead.start(R.lo, a.T, a.H, R.h);
+  at = ahead;
+  auto issue = [&](int st) {
+    const uint32_t n = row_bytes<E, VEC>(ahead.row, d, total_rows);
+    const uint32_t slot = smem_u32(smem) + st * nsrc * rg.slot, bar = smem_u32(&bars.full[st]);
+    mbar_arrive_expect_tx(bar, n * nsrc);
+    row_copy(slot, X, ahead.row, d, n, bar);
+    if (Rs) row_copy(slot + rg.slot, Rs, ahead.row, d, n, bar);
+    ahead.next(1, a.T, a.H);
+  };
+  if (tid == 0)
+    for (int s = 0; s < rg.stages && ahead.i < R.hi; ++s) issue(s);
+  float2 w[F::NP], bb[F::NP];
+  f.get_f32(a.weight ? a.weight + (size_t)R.h * d : nullptr, 1.f, w);
+  f.get_f32(a.bias ? a.bias + (size_t)R.h * d : nullptr, 0.f, bb);
+  int st = 0;
+  uint32_t ph = 0;
+  for (; at.i < R.hi; at.next(1, a.T, a.H)) {
+    const size_t row = at.row;
+    const RowView rv = row_view<E, VEC>(row, d, total_rows);
+    const uint8_t* slot = smem + st * nsrc * rg.slot;
+    // a wait that runs out is recorded; the loop goes on without waiting, so that all threads
+    // keep meeting at the barriers
+    mbar_wait(smem_u32(&bars.full[st]), ph, ab);
+    float2 v[F::NP];
+    float t[1];
+    slot_read(f, slot, rv, X + row * d, v);
+    if (Rs) {
+      float2 r[F::NP];
+      slot_read(f, slot + rg.slot, rv, Rs + row * d, r);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        join[grp * W + col[n] + k] = dw[n][k];
-        join[kNarrowThreads * NV * VEC + grp * W + col[n] + k] = db[n][k];
-      }
-    __syncthreads();
-    for (int j = threadIdx.x; j < d; j += kNarrowThreads) {
-      float tw = 0.f, tb = 0.f;
-#pragma unroll
-      for (int g = 0; g < kNarrowThreads / G; ++g) {
-        tw += join[g * W + j];
-        tb += join[kNarrowThreads * NV * VEC + g * W + j];
-      }
-      if (pt.dw0) pt.dw0[base + j] = tw;
-      if (pt.db0) pt.db0[base + j] = tb;
+      for (int i = 0; i < F::NP; ++i) v[i] = add2(v[i], r[i]);
+    }
+    t[0] = total(v);
+    cta_sum(t, bars.red[0]);
+    if (tid == 0 && ahead.i < R.hi) issue(st);
+    if (++st == rg.stages) { st = 0; ph ^= 1; }
+    const float mean = t[0] * inv_d;
+    if (S) f.store(S + row * d, v);
+    f.centre(mean, v);
+    t[0] = total_sq(v);
+    cta_sum(t, bars.red[1]);
+    const float rstd = rsqrtf(fmaf(t[0], inv_d, a.eps));
+    scale_shift(rstd, w, bb, v);
+    f.store(Y + y_row(a, R, at) * d, v);
+    if (tid == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
     }
   }
+}
+
+// RU rows per step share one barrier; a stage is refilled behind the next step's barrier, so that
+// dS is read from it after the sums instead of being held in registers.
+template <typename E, int VEC, int NV, int RU, int MAXT>
+__global__ void __launch_bounds__(MAXT, 640 / MAXT)
+    norm_bwd_wide(const __grid_constant__ NormArgs a, const Split sp, const Ring rg,
+                  const Partials pt) {
+  using F = Frag<E, VEC, NV>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ RingBars bars;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const Rows R(a, sp);
+  const int tid = threadIdx.x, d = a.d;
+  const F f{tid * VEC, (int)blockDim.x * VEC, d};
+  const float inv_d = 1.f / (float)d;
+  const size_t total_rows = (size_t)a.B * a.H * a.T;
+  const E* X = static_cast<const E*>(a.X);
+  const E* dY = static_cast<const E*>(a.dY);
+  const E* dS = static_cast<const E*>(a.dS);
+  E* dX = static_cast<E*>(a.dX);
+  const Abort ab{&bars.abort_flag, a.err};
+  const int nsrc = dS ? 3 : 2;
+  ring_init(bars, rg);
+  Walk ahead, at;
+  ahead.start(R.lo, a.T, a.H, R.h);
+  at = ahead;
+  int ist = 0;  // the stage that the next row loads into
+  auto issue = [&](int n) {
+    for (; n > 0 && ahead.i < R.hi; --n) {
+      const size_t yrow = y_row(a, R, ahead);
+      const uint32_t nx = row_bytes<E, VEC>(ahead.row, d, total_rows);
+      const uint32_t ny = row_bytes<E, VEC>(yrow, d, total_rows);
+      const uint32_t slot = smem_u32(smem) + ist * nsrc * rg.slot;
+      const uint32_t bar = smem_u32(&bars.full[ist]);
+      mbar_arrive_expect_tx(bar, nx * (nsrc - 1) + ny);
+      row_copy(slot, X, ahead.row, d, nx, bar);
+      row_copy(slot + rg.slot, dY, yrow, d, ny, bar);
+      if (dS) row_copy(slot + 2 * rg.slot, dS, ahead.row, d, nx, bar);
+      ahead.next(1, a.T, a.H);
+      if (++ist == rg.stages) ist = 0;
+    }
+  };
+  if (tid == 0) issue(rg.stages);
+  float2 w[F::NP], dw[F::NP], db[F::NP];
+  f.get_f32(a.weight ? a.weight + (size_t)R.h * d : nullptr, 1.f, w);
+#pragma unroll
+  for (int i = 0; i < F::NP; ++i) dw[i] = db[i] = both(0.f);
+  int st = 0, buf = 0;
+  uint32_t ph = 0;
+  float mean[RU], rstd[RU], nmean[RU], nrstd[RU];
+  Walk stat = at;  // the row whose statistics are read next
+  auto stats = [&]() {
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      nmean[u] = nrstd[u] = 0.f;
+      if (stat.i < R.hi) {
+        nmean[u] = a.mean[stat.row];
+        nrstd[u] = a.rstd[stat.row];
+      }
+      stat.next(1, a.T, a.H);
+    }
+  };
+  stats();
+  const bool tight = rg.stages < 2 * RU;
+  for (bool first = true; at.i < R.hi; first = false) {  // uniform over the CTA
+    float2 xh[RU][F::NP], g[RU][F::NP];
+    float t[2 * RU];
+    size_t row[RU];
+    const uint8_t* slot[RU];
+    bool live[RU];
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      live[u] = at.i < R.hi;
+      row[u] = at.row;
+      slot[u] = smem + st * nsrc * rg.slot;
+      mean[u] = nmean[u];
+      rstd[u] = nrstd[u];
+      t[2 * u] = t[2 * u + 1] = 0.f;
+      if (live[u]) {
+        const size_t yrow = y_row(a, R, at);
+        // a wait that runs out is recorded; the loop goes on without waiting, so that all
+        // threads keep meeting at the barriers
+        mbar_wait(smem_u32(&bars.full[st]), ph, ab);
+        slot_read(f, slot[u], row_view<E, VEC>(row[u], d, total_rows), X + row[u] * d, xh[u]);
+        slot_read(f, slot[u] + rg.slot, row_view<E, VEC>(yrow, d, total_rows), dY + yrow * d, g[u]);
+        bwd_first(mean[u], rstd[u], w, xh[u], g[u], dw, db, t[2 * u], t[2 * u + 1]);
+        if (++st == rg.stages) { st = 0; ph ^= 1; }
+      }
+      at.next(1, a.T, a.H);
+    }
+    stats();
+    cta_sum(t, bars.red[buf]);
+    buf ^= 1;
+    if (tid == 0 && !first && !tight) issue(RU);  // the last step's rows are all done with
+#pragma unroll
+    for (int u = 0; u < RU; ++u)
+      if (live[u]) {
+        bwd_second(rstd[u], t[2 * u] * inv_d, t[2 * u + 1] * inv_d, xh[u], g[u]);
+        if (dS) {
+          float2 s[F::NP];
+          slot_read(f, slot[u] + 2 * rg.slot, row_view<E, VEC>(row[u], d, total_rows),
+                    dS + row[u] * d, s);
+#pragma unroll
+          for (int i = 0; i < F::NP; ++i) g[u][i] = add2(g[u][i], s[i]);
+        }
+        f.store(dX + row[u] * d, g[u]);
+      }
+    if (tight) {
+      __syncthreads();
+      if (tid == 0) issue(RU);
+    }
+  }
+  const size_t base = R.s * pt.ldp + (size_t)R.h * d;
+  f.each_f32([&](int i, int h, int c) {
+    if (pt.dw0) pt.dw0[base + c] = h ? dw[i].y : dw[i].x;
+    if (pt.db0) pt.db0[base + c] = h ? db[i].y : db[i].x;
+  });
 }
 
 // dweight[j] = sum over s of part[s][0][j], dbias likewise from part[s][1]: 32 columns per CTA,
@@ -406,7 +767,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 // ------------------------------------------------------------------------------ launch rules
 struct Shape {
-  int vec, nv, g, threads;  // g = 0: one CTA of `threads` per row
+  int vec, nv, g, threads;  // g = 0: a wide row, one CTA of `threads`
 };
 // Narrow rows take as few lanes as hold the row in at most two (scalar: eight) accesses each;
 // wide rows one access per thread up to 512 threads, then more accesses.
@@ -414,7 +775,7 @@ Shape shape_of(const NormArgs& a) {
   const int v = a.bf16 ? 8 : 4;
   Shape s;
   s.vec = a.d % v == 0 ? v : 1;
-  const int n = (a.d + s.vec - 1) / s.vec;
+  const int n = a.d / s.vec;
   s.threads = kNarrowThreads;
   if (s.vec > 1) {
     if (n <= 8) { s.g = 8; s.nv = 1; return s; }
@@ -433,78 +794,139 @@ Shape shape_of(const NormArgs& a) {
   return s;
 }
 
-// CTAs that run at once, from the threads of an SM that the kernels' registers allow.
-Split split_of(const NormArgs& a, const Shape& sh, int threads_per_sm, int min_rows) {
+// CTAs of an SM, from the threads that the kernels' registers leave room for.
+int ctas_per_sm(const Shape& sh, bool bwd) {
+  const int threads = sh.g ? (bwd ? 512 : 640) : sh.nv > 2 ? 512 : bwd ? 640 : 1024;
+  return std::max(1, std::min(8, threads / sh.threads));
+}
+// A run of the backward has at least four rows per group, so that the shares of the weight
+// gradients it writes are few against the rows it reads.
+Split split_of(const NormArgs& a, const Shape& sh, bool bwd) {
+  const int min_rows = bwd ? 4 : 1;
   const long long bt = (long long)a.B * a.T;
   const int ngrp = sh.g ? kNarrowThreads / sh.g : 1;
-  const long long slots = (long long)kSMs * std::max(1, threads_per_sm / sh.threads);
+  const long long slots = (long long)kSMs * ctas_per_sm(sh, bwd);
   // every SM gets a CTA before any run is longer than one row per group; beyond that a run has
   // at least min_rows per group
   const long long one = (bt + ngrp - 1) / ngrp, few = (one + min_rows - 1) / min_rows;
-  long long S = std::min(std::max(1ll, slots / a.H),
-                         std::max(few, std::min(one, (long long)(kSMs + a.H - 1) / a.H)));
-  Split sp;
-  sp.L = (int)((bt + S - 1) / S);
-  sp.L = (int)std::min(bt, (long long)(sp.L + ngrp - 1) / ngrp * ngrp);
+  const long long S = std::min(std::max(1ll, slots / a.H),
+                               std::max(few, std::min(one, (long long)(kSMs + a.H - 1) / a.H)));
+  Split sp{};
+  const long long L = (bt + S - 1) / S;
+  sp.L = (int)std::min(bt, (L + ngrp - 1) / ngrp * ngrp);
   sp.S = (int)((bt + sp.L - 1) / sp.L);
   return sp;
 }
-Split fwd_split(const NormArgs& a, const Shape& sh) { return split_of(a, sh, 1024, 1); }
-Split bwd_split(const NormArgs& a, const Shape& sh) { return split_of(a, sh, 640, 4); }
+Split fwd_split(const NormArgs& a, const Shape& sh) { return split_of(a, sh, false); }
+Split bwd_split(const NormArgs& a, const Shape& sh) { return split_of(a, sh, true); }
 
-template <typename E, int VEC, int NV, int G>
-void launch_fwd(const NormArgs& a, const Shape& sh, cudaStream_t s) {
-  const Split sp = fwd_split(a, sh);
-  norm_fwd_kernel<E, VEC, NV, G><<<(unsigned)a.H * sp.S, sh.threads, 0, s>>>(a, sp);
+constexpr uint32_t kRingBytes = 200 << 10;  // of an SM's shared memory, for all its CTAs
+Ring ring_of(const NormArgs& a, const Shape& sh, int nsrc, bool bwd) {
+  const uint32_t es = a.bf16 ? 2 : 4;
+  Ring r;
+  // off a 16-byte boundary a row touches up to one block more on each side
+  r.slot = sh.vec > 1 ? a.d * es : (a.d * es + 30) / 16 * 16;
+  const uint32_t room = kRingBytes / ctas_per_sm(sh, bwd) / (nsrc * r.slot);
+  r.stages = (int)std::max(1u, std::min((uint32_t)kMaxStages, room));
+  return r;
 }
-template <typename E, int VEC, int NV, int G>
-void launch_bwd(const NormArgs& a, const Shape& sh, cudaStream_t s) {
-  const Split sp = bwd_split(a, sh);
+template <typename K>
+cudaError_t ring_room(K kernel, size_t smem) {
+  return smem > (40 << 10) ? cudaFuncSetAttribute(
+             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
+}
+
+Partials partials_of(const NormArgs& a, const Split& sp) {
   const size_t cols = (size_t)a.H * a.d;
-  Partials pt{};
-  if (a.dweight || a.dbias) {
-    float* ws = static_cast<float*>(a.ws);
-    pt = sp.S == 1 ? Partials{a.dweight, a.dbias, 0} : Partials{ws, ws + cols, 2 * cols};
-  }
-  norm_bwd_kernel<E, VEC, NV, G><<<(unsigned)a.H * sp.S, sh.threads, 0, s>>>(a, sp, pt);
+  if (!a.dweight && !a.dbias) return {};
+  if (sp.S == 1) return {a.dweight, a.dbias, 0};
+  float* ws = static_cast<float*>(a.ws);
+  return {ws, ws + cols, 2 * cols};
 }
 
-// Calls F::run<E, VEC, NV, G>(a, sh, s) for the shape's instance.
-#define NORM_DISPATCH(F)                                                                     \
-  do {                                                                                       \
-    const Shape sh = shape_of(a);                                                            \
-    if (a.bf16 && sh.vec == 8) {                                                             \
-      if (sh.g == 8) F<bf16, 8, 1, 8>(a, sh, s);                                             \
-      else if (sh.g == 16) F<bf16, 8, 1, 16>(a, sh, s);                                      \
-      else if (sh.g == 32 && sh.nv == 1) F<bf16, 8, 1, 32>(a, sh, s);                        \
-      else if (sh.g == 32) F<bf16, 8, 2, 32>(a, sh, s);                                      \
-      else if (sh.nv == 1) F<bf16, 8, 1, 0>(a, sh, s);                                       \
-      else if (sh.nv == 2) F<bf16, 8, 2, 0>(a, sh, s);                                       \
-      else F<bf16, 8, 4, 0>(a, sh, s);                                                       \
-    } else if (!a.bf16 && sh.vec == 4) {                                                     \
-      if (sh.g == 8) F<float, 4, 1, 8>(a, sh, s);                                            \
-      else if (sh.g == 16) F<float, 4, 1, 16>(a, sh, s);                                     \
-      else if (sh.g == 32 && sh.nv == 1) F<float, 4, 1, 32>(a, sh, s);                       \
-      else if (sh.g == 32) F<float, 4, 2, 32>(a, sh, s);                                     \
-      else if (sh.nv == 1) F<float, 4, 1, 0>(a, sh, s);                                      \
-      else if (sh.nv == 2) F<float, 4, 2, 0>(a, sh, s);                                      \
-      else if (sh.nv == 4) F<float, 4, 4, 0>(a, sh, s);                                      \
-      else F<float, 4, 8, 0>(a, sh, s);                                                      \
-    } else if (a.bf16) {                                                                     \
-      NORM_SCALAR(F, bf16);                                                                  \
-    } else {                                                                                 \
-      NORM_SCALAR(F, float);                                                                 \
-    }                                                                                        \
-  } while (0)
-#define NORM_SCALAR(F, E)                                                                    \
-  do {                                                                                       \
-    if (sh.g == 32 && sh.nv == 1) F<E, 1, 1, 32>(a, sh, s);                                  \
-    else if (sh.g == 32 && sh.nv == 4) F<E, 1, 4, 32>(a, sh, s);                             \
-    else if (sh.g == 32) F<E, 1, 8, 32>(a, sh, s);                                           \
-    else if (sh.nv == 4) F<E, 1, 4, 0>(a, sh, s);                                            \
-    else if (sh.nv == 8) F<E, 1, 8, 0>(a, sh, s);                                            \
-    else F<E, 1, 32, 0>(a, sh, s);                                                           \
-  } while (0)
+struct Fwd {
+  template <typename E, int VEC, int NV, int G, int RU>
+  static cudaError_t narrow(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+    const Split sp = fwd_split(a, sh);
+    const unsigned grid = (unsigned)a.H * sp.S;
+    if (a.residual)
+      norm_fwd_narrow<E, VEC, NV, G, RU, true><<<grid, sh.threads, 0, s>>>(a, sp);
+    else
+      norm_fwd_narrow<E, VEC, NV, G, 2 * RU, false><<<grid, sh.threads, 0, s>>>(a, sp);
+    return cudaGetLastError();
+  }
+  template <typename E, int VEC, int NV>
+  static cudaError_t wide(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+    const Split sp = fwd_split(a, sh);
+    const int nsrc = a.residual ? 2 : 1;
+    const Ring rg = ring_of(a, sh, nsrc, false);
+    const size_t smem = (size_t)rg.stages * nsrc * rg.slot;
+    const cudaError_t e = ring_room(norm_fwd_wide<E, VEC, NV>, smem);
+    if (e != cudaSuccess) return e;
+    norm_fwd_wide<E, VEC, NV><<<(unsigned)a.H * sp.S, sh.threads, smem, s>>>(a, sp, rg);
+    return cudaGetLastError();
+  }
+};
+struct Bwd {
+  template <typename E, int VEC, int NV, int G, int RU>
+  static cudaError_t narrow(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+    const Split sp = bwd_split(a, sh);
+    norm_bwd_narrow<E, VEC, NV, G, RU>
+        <<<(unsigned)a.H * sp.S, sh.threads, 0, s>>>(a, sp, partials_of(a, sp));
+    return cudaGetLastError();
+  }
+  template <typename E, int VEC, int NV>
+  static cudaError_t wide(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+    const Split sp = bwd_split(a, sh);
+    const int nsrc = a.dS ? 3 : 2;
+    const Ring rg = ring_of(a, sh, nsrc, true);
+    const size_t smem = (size_t)rg.stages * nsrc * rg.slot;
+    if constexpr (NV == 1) {
+      if (sh.threads <= 320) return wide_launch(norm_bwd_wide<E, VEC, 1, 2, 320>, a, sh, sp, rg, smem, s);
+    }
+    return wide_launch(norm_bwd_wide<E, VEC, NV, NV == 1 ? 2 : 1, 512>, a, sh, sp, rg, smem, s);
+  }
+  template <typename K>
+  static cudaError_t wide_launch(K kernel, const NormArgs& a, const Shape& sh, const Split& sp,
+                                 const Ring& rg, size_t smem, cudaStream_t s) {
+    const cudaError_t e = ring_room(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)a.H * sp.S, sh.threads, smem, s>>>(a, sp, rg, partials_of(a, sp));
+    return cudaGetLastError();
+  }
+};
+
+// The instance of a row shape. RU (rows per group and step; twice that in a forward without
+// residual) is what the registers leave room for.
+template <typename F, typename E, int VEC>
+cudaError_t dispatch_vec(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+  if (sh.g == 8) return F::template narrow<E, VEC, 1, 8, 2>(a, sh, s);
+  if (sh.g == 16) return F::template narrow<E, VEC, 1, 16, 2>(a, sh, s);
+  if (sh.g == 32 && sh.nv == 1) return F::template narrow<E, VEC, 1, 32, 2>(a, sh, s);
+  if (sh.g == 32) return F::template narrow<E, VEC, 2, 32, 1>(a, sh, s);
+  if (sh.nv == 1) return F::template wide<E, VEC, 1>(a, sh, s);
+  if (sh.nv == 2) return F::template wide<E, VEC, 2>(a, sh, s);
+  if (sh.nv == 4) return F::template wide<E, VEC, 4>(a, sh, s);
+  if constexpr (VEC == 4) return F::template wide<E, VEC, 8>(a, sh, s);  // float32 rows only
+  return cudaErrorInvalidValue;
+}
+template <typename F, typename E>
+cudaError_t dispatch_scalar(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+  if (sh.g == 32 && sh.nv == 1) return F::template narrow<E, 1, 1, 32, 2>(a, sh, s);
+  if (sh.g == 32 && sh.nv == 4) return F::template narrow<E, 1, 4, 32, 2>(a, sh, s);
+  if (sh.g == 32) return F::template narrow<E, 1, 8, 32, 1>(a, sh, s);
+  if (sh.nv == 4) return F::template wide<E, 1, 4>(a, sh, s);
+  if (sh.nv == 8) return F::template wide<E, 1, 8>(a, sh, s);
+  return F::template wide<E, 1, 32>(a, sh, s);
+}
+template <typename F>
+cudaError_t dispatch(const NormArgs& a, cudaStream_t s) {
+  const Shape sh = shape_of(a);
+  count_launches(1);
+  if (sh.vec == 8) return dispatch_vec<F, bf16, 8>(a, sh, s);
+  if (sh.vec == 4) return dispatch_vec<F, float, 4>(a, sh, s);
+  return a.bf16 ? dispatch_scalar<F, bf16>(a, sh, s) : dispatch_scalar<F, float>(a, sh, s);
+}
 
 }  // namespace
 
@@ -515,16 +937,10 @@ size_t norm_bwd_workspace(const NormArgs& a) {
   return sp.S == 1 ? 0 : (size_t)sp.S * 2 * a.H * a.d * sizeof(float);
 }
 
-cudaError_t norm_fwd(const NormArgs& a, cudaStream_t s) {
-  NORM_DISPATCH(launch_fwd);
-  count_launches(1);
-  return cudaGetLastError();
-}
+cudaError_t norm_fwd(const NormArgs& a, cudaStream_t s) { return dispatch<Fwd>(a, s); }
 
 cudaError_t norm_bwd(const NormArgs& a, cudaStream_t s) {
-  NORM_DISPATCH(launch_bwd);
-  count_launches(1);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = dispatch<Bwd>(a, s);
   const Split sp = bwd_split(a, shape_of(a));
   if (e != cudaSuccess || sp.S == 1 || !(a.dweight || a.dbias)) return e;
   const size_t cols = (size_t)a.H * a.d;

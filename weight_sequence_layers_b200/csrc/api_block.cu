@@ -114,6 +114,8 @@ ttt_status ttt_recur_fwd(const ttt_recur_config* cfg, const void* X, const void*
   if (!X || !G || !H) return TTT_ERR_INVALID_ARG;
   if (!aligned16({X, G, reset, h0, H, h_final})) return TTT_ERR_ALIGNMENT;
   a.X = X; a.G = G; a.reset = reset; a.h0 = h0; a.H = H; a.h_final = h_final;
+  a.err = current_error_word();
+  if (!a.err) return TTT_ERR_CUDA;
   return status_of(recur_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -128,6 +130,8 @@ ttt_status ttt_recur_bwd(const ttt_recur_config* cfg, const void* X, const void*
   if (!aligned16({X, G, reset, h0, H, dH, dh_final, dX, dG, dh0})) return TTT_ERR_ALIGNMENT;
   a.X = X; a.G = G; a.reset = reset; a.h0 = h0; a.H_in = H; a.dH = dH; a.dh_final = dh_final;
   a.dX = dX; a.dG = dG; a.dh0 = dh0;
+  a.err = current_error_word();
+  if (!a.err) return TTT_ERR_CUDA;
   return status_of(recur_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "simt_util.cuh"
 
@@ -26,33 +27,6 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kSMs = 148;
 constexpr int kNarrowThreads = 128;  // CTA of the narrow-row kernels
-
-// Pairs of float32 in one instruction (add, mul, fma on f32x2): the kernels are bound by the
-// instructions they issue before they are by HBM (a 16-byte access holds eight bf16), and a pair
-// costs one issue slot.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 c;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(c.x), "=f"(c.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return c;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 c;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(c.x), "=f"(c.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return c;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 d) {
-  float2 c;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(c.x), "=f"(c.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(d.x), "f"(d.y));
-  return c;
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // VEC elements of a row: one 16-byte access, or one element where the width does not keep rows
 // on 16-byte boundaries. Coherent loads, since S may be X or residual and dX may be dS.

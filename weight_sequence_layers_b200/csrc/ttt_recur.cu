@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "simt_util.cuh"
 
@@ -32,15 +33,55 @@ constexpr int kSMs = 148;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
 
+// A thread's features of one token: one float, or two in a pair (f32x2 arithmetic).
+template <int VC>
+struct VecOf { using T = float; };
+template <>
+struct VecOf<2> { using T = float2; };
+template <int VC>
+using Vec = typename VecOf<VC>::T;
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return add2(a, b); }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return mul2(a, b); }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return fma2(a, b, c); }
+template <int VC>
+__device__ __forceinline__ Vec<VC> all(float v) {
+  if constexpr (VC == 1) return v;
+  else return both(v);
+}
+template <typename V>
+__device__ __forceinline__ V pick(bool c, V a, V b) {
+  if constexpr (sizeof(V) == 4) return c ? a : b;
+  else return make_float2(c ? a.x : b.x, c ? a.y : b.y);
+}
+
 // a = sigmoid(g) = 1 / (1 + e) and 1 - a = e a with e = exp(-g): neither is a difference. e is
 // held at 2^126, where a is the smallest normal number and 1 - a is 1; a NaN stays one.
-__device__ __forceinline__ void gate_of(float g, float& a, float& na) {
-  float x = g * -1.44269504f, e, r;
-  asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x));  // 126
+__device__ __forceinline__ float exp2_held(float x) {
+  float e;
+  asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(x) : "f"(x));  // 126
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  a = r;
-  na = e * r;
+  return e;
+}
+__device__ __forceinline__ float recip(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kNegLog2e = -1.44269504f;
+__device__ __forceinline__ void gate_of(float g, float& a, float& na) {
+  const float e = exp2_held(g * kNegLog2e);
+  a = recip(1.f + e);
+  na = e * a;
+}
+__device__ __forceinline__ void gate_of(float2 g, float2& a, float2& na) {
+  const float2 x = mul2(g, both(kNegLog2e));
+  const float2 e = make_float2(exp2_held(x.x), exp2_held(x.y));
+  const float2 q = add2(e, both(1.f));
+  a = make_float2(recip(q.x), recip(q.y));
+  na = mul2(e, a);
 }
 
 // VC neighbouring elements of a row as they lie in memory.
@@ -52,8 +93,8 @@ struct Raw<bf16, 1> {
   __device__ __forceinline__ void load(const bf16* p) {
     asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
   }
-  __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)r << 16); }
-  static __device__ __forceinline__ void store(bf16* p, const float* v) { *p = __float2bfloat16_rn(v[0]); }
+  __device__ __forceinline__ float get() const { return __uint_as_float((uint32_t)r << 16); }
+  static __device__ __forceinline__ void store(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
 template <>
 struct Raw<bf16, 2> {
@@ -61,9 +102,9 @@ struct Raw<bf16, 2> {
   __device__ __forceinline__ void load(const bf16* p) {
     asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r) : "l"(p));
   }
-  __device__ __forceinline__ float get(int k) const { return k ? bf16hi(r) : bf16lo(r); }
-  static __device__ __forceinline__ void store(bf16* p, const float* v) {
-    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+  __device__ __forceinline__ float2 get() const { return make_float2(bf16lo(r), bf16hi(r)); }
+  static __device__ __forceinline__ void store(bf16* p, float2 v) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
   }
 };
 template <>
@@ -72,8 +113,8 @@ struct Raw<float, 1> {
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.L1::no_allocate.f32 %0, [%1];" : "=f"(r) : "l"(p));
   }
-  __device__ __forceinline__ float get(int) const { return r; }
-  static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
+  __device__ __forceinline__ float get() const { return r; }
+  static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 };
 template <>
 struct Raw<float, 2> {
@@ -81,21 +122,32 @@ struct Raw<float, 2> {
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.L1::no_allocate.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "l"(p));
   }
-  __device__ __forceinline__ float get(int k) const { return k ? r.y : r.x; }
-  static __device__ __forceinline__ void store(float* p, const float* v) {
-    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-  }
+  __device__ __forceinline__ float2 get() const { return r; }
+  static __device__ __forceinline__ void store(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 };
+// i rows of D elements (i a constant: one wide multiply-add on the pointer).
+template <typename E>
+__device__ __forceinline__ E* rows(E* p, int i, unsigned D) {
+  return reinterpret_cast<E*>(reinterpret_cast<uintptr_t>(p) +
+                              (uint64_t)D * (uint32_t)(i * sizeof(E)));
+}
+template <typename E>
+__device__ __forceinline__ E* rows_back(E* p, int i, unsigned D) {
+  return reinterpret_cast<E*>(reinterpret_cast<uintptr_t>(p) -
+                              (uint64_t)D * (uint32_t)(i * sizeof(E)));
+}
 
 // ------------------------------------------------------------------------------------- joins
 template <int VC>
 struct __align__(8 * VC) Map {
-  float A[VC], U[VC];
+  Vec<VC> A, U;
 };
 template <int VC>
 struct Joins {  // two buffers in turn: a buffer is written again two joins later
   Map<VC> seg[2][kWarps][32], cta[2][kMaxCluster][32];
   unsigned seg_reset[2][kWarps], cta_reset[2][kMaxCluster];
+  uint64_t full[2];  // the cluster's maps of the round have arrived in cta and cta_reset
+  int abort_flag;
 };
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -107,78 +159,108 @@ __device__ __forceinline__ uint32_t remote(uint32_t addr, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// Stores to a CTA of the cluster that count their bytes on its barrier: the receiver waits for
+// the data alone, where a release would make every round wait for the outputs' stores too.
+__device__ __forceinline__ void st_async(uint32_t addr, const Map<1>& m, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1,%2}, [%3];"
+               ::"r"(addr), "f"(m.A), "f"(m.U), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t addr, const Map<2>& m, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], "
+               "{%1,%2,%3,%4}, [%5];" ::"r"(addr), "f"(m.A.x), "f"(m.A.y), "f"(m.U.x), "f"(m.U.y),
+               "r"(bar) : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];"
+               ::"r"(addr), "r"(v), "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// As mbar_wait; a wait that runs out is recorded, and the rounds go on without waiting.
+__device__ __forceinline__ void wait_cluster(uint32_t bar, uint32_t parity, const Abort& ab) {
+  if (try_wait_cluster(bar, parity) || *ab.flag) return;
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t it = 1; !try_wait_cluster(bar, parity); ++it)
+    if ((it & 63u) == 0 && (*ab.flag || globaltimer() - t0 > kWaitLimitNs)) {
+      if (!*ab.flag) atomicOr(ab.err, ERR_WAIT_TIMEOUT);
+      *ab.flag = 1;
+      return;
+    }
+}
+// Before the first join: the barriers, and that all CTAs of the cluster have started.
 template <int VC>
-__device__ __forceinline__ void st_remote(uint32_t addr, const Map<VC>& m) {
-#pragma unroll
-  for (int k = 0; k < VC; ++k) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr + 4 * k), "f"(m.A[k]) : "memory");
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr + 4 * (VC + k)), "f"(m.U[k]) : "memory");
+__device__ __forceinline__ void join_init(Joins<VC>& js, int cl) {
+  if (cl == 1) return;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&js.full[0]), 1);
+    mbar_init(smem_u32(&js.full[1]), 1);
+    js.abort_flag = 0;
+    fence_barrier_init();
   }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// h through maps 0..n-1 in order; `in` is h before map `mine`. resets: bit s for map s.
+template <int VC, int N>
+__device__ __forceinline__ void fold(const Map<VC> (*maps)[32], int n, unsigned resets, int mine,
+                                     Vec<VC>& h, Vec<VC>& in) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 0; s < N; ++s)
+    if (s < n) {
+      const Map<VC> q = maps[s][lane];
+      if (s == mine) in = h;
+      h = fma(q.A, h, q.U);
+      if (resets >> s & 1) h = q.U;
+    }
 }
 
 // Joins the warps' maps m (reset: it holds a document's first token) of one round: `carry` goes
-// from the state that enters the round to the one that leaves it, `in` is the state that enters
+// from the state that enters the round to the one that leaves it; returns the state that enters
 // this warp's run. All threads of the cluster call it the same number of times.
+// A buffer of `cta` is free again when the next round's maps arrive: a CTA sends those behind
+// the barrier that all its threads reach after reading it, and sends into the buffer again only
+// after it has them from all.
 template <int VC>
-__device__ __forceinline__ void join_runs(Joins<VC>& js, int buf, int cl, int rank,
-                                          const Map<VC>& m, bool reset, float (&carry)[VC],
-                                          float (&in)[VC]) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int cl, int rank,
+                                             const Map<VC>& m, bool reset, Vec<VC>& carry,
+                                             unsigned* err) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = round & 1;
   js.seg[buf][w][lane] = m;
   if (lane == 0) js.seg_reset[buf][w] = reset;
+  const uint32_t full = smem_u32(&js.full[buf]);
+  if (cl > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(full, cl * (32 * sizeof(Map<VC>) + 4));
   __syncthreads();
   const unsigned rs = __ballot_sync(~0u, lane < kWarps && js.seg_reset[buf][lane & (kWarps - 1)]);
-  float h[VC];
-#pragma unroll
-  for (int k = 0; k < VC; ++k) h[k] = carry[k];
+  Vec<VC> h = carry, in = carry;
   if (cl > 1) {
-    Map<VC> c;
-#pragma unroll
-    for (int k = 0; k < VC; ++k) c.A[k] = 1.f, c.U[k] = 0.f;
-#pragma unroll
-    for (int s = 0; s < kWarps; ++s) {
-      const Map<VC> q = js.seg[buf][s][lane];
-#pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        c.A[k] *= q.A[k];
-        c.U[k] = rs >> s & 1 ? q.U[k] : fmaf(q.A[k], c.U[k], q.U[k]);
-      }
-    }
     if (w < cl) {  // warp w hands the CTA's map to CTA w
-      st_remote(remote(smem_u32(&js.cta[buf][rank][lane]), w), c);
-      if (lane == 0)
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                         remote(smem_u32(&js.cta_reset[buf][rank]), w)), "r"(rs) : "memory");
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][lane & (kMaxCluster - 1)]);
-    for (int s = 0; s < cl; ++s) {
-      const Map<VC> q = js.cta[buf][s][lane];
+      Map<VC> c{all<VC>(1.f), all<VC>(0.f)};
 #pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        if (s == rank) in[k] = h[k];
-        h[k] = crs >> s & 1 ? q.U[k] : fmaf(q.A[k], h[k], q.U[k]);
+      for (int s = 0; s < kWarps; ++s) {
+        const Map<VC> q = js.seg[buf][s][lane];
+        c.A = mul(c.A, q.A);
+        c.U = fma(q.A, c.U, q.U);
+        if (rs >> s & 1) c.U = q.U;
       }
+      const uint32_t bar = remote(full, w);
+      st_async(remote(smem_u32(&js.cta[buf][rank][lane]), w), c, bar);
+      if (lane == 0) st_async(remote(smem_u32(&js.cta_reset[buf][rank]), w), rs, bar);
     }
-#pragma unroll
-    for (int k = 0; k < VC; ++k) {
-      carry[k] = h[k];
-      h[k] = in[k];
-    }
+    wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
+    const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][lane & (kMaxCluster - 1)]);
+    fold<VC, kMaxCluster>(js.cta[buf], cl, crs, rank, h, in);
+    carry = h;
+    h = in;
   }
-#pragma unroll
-  for (int s = 0; s < kWarps; ++s) {
-    const Map<VC> q = js.seg[buf][s][lane];
-#pragma unroll
-    for (int k = 0; k < VC; ++k) {
-      if (s == w) in[k] = h[k];
-      h[k] = rs >> s & 1 ? q.U[k] : fmaf(q.A[k], h[k], q.U[k]);
-    }
-  }
-  if (cl == 1)
-#pragma unroll
-    for (int k = 0; k < VC; ++k) carry[k] = h[k];
+  fold<VC, kWarps>(js.seg[buf], kWarps, rs, w, h, in);
+  if (cl == 1) carry = h;
+  return in;
 }
 
 // This thread's place: features c.. of batch row b, run w of CTA `rank` of the cluster.
@@ -195,27 +277,22 @@ struct Place {
     ok = c < a.D;
   }
 };
-// A CTA's shared memory may be written by the others once all have started.
-__device__ __forceinline__ void cluster_sync(int cl) {
-  if (cl == 1) return;
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 template <int VC>
-__device__ __forceinline__ void load_state(const float* p, const RecurArgs& a, const Place<VC>& at,
-                                           float (&v)[VC]) {
-#pragma unroll
-  for (int k = 0; k < VC; ++k) v[k] = p && at.ok ? p[(size_t)at.b * a.D + at.c + k] : 0.f;
+__device__ __forceinline__ Vec<VC> load_state(const float* p, const RecurArgs& a,
+                                              const Place<VC>& at) {
+  if (!p || !at.ok) return all<VC>(0.f);
+  p += (size_t)at.b * a.D + at.c;
+  if constexpr (VC == 1) return *p;
+  else return make_float2(p[0], p[1]);
 }
 template <int VC>
 __device__ __forceinline__ void store_state(float* p, const RecurArgs& a, const Place<VC>& at,
-                                            const float (&v)[VC]) {
+                                            Vec<VC> v) {
   if (p && at.ok && at.rank == 0 && threadIdx.x < 32)
-#pragma unroll
-    for (int k = 0; k < VC; ++k) p[(size_t)at.b * a.D + at.c + k] = v[k];
+    Raw<float, VC>::store(p + (size_t)at.b * a.D + at.c, v);
 }
-// R documents' marks from position pos of a walk (position p is token p, or T - 1 - p with REV):
-// lane i loads that of position pos + i.
+// The documents' marks of R positions from pos of a walk (position p is token p, or T - 1 - p
+// with REV): lane i loads that of position pos + i.
 template <int R, bool REV>
 __device__ __forceinline__ unsigned load_reset(const RecurArgs& a, int b, unsigned pos) {
   const unsigned p = pos + (threadIdx.x & 31);
@@ -227,10 +304,11 @@ __device__ __forceinline__ unsigned load_reset(const RecurArgs& a, int b, unsign
 template <typename E, typename GT, bool SIG, int VC, int R, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS)
     recur_fwd_kernel(const __grid_constant__ RecurArgs a, const int cluster) {
+  using V = Vec<VC>;
   __shared__ Joins<VC> js;
   const Place<VC> at(a, cluster);
-  const unsigned T = a.T, stride = (unsigned)at.cl * kWarps * R;
-  const size_t D = a.D, base = (size_t)at.b * T * D + at.c;
+  const unsigned T = a.T, D = a.D, stride = (unsigned)at.cl * kWarps * R;
+  const size_t base = (size_t)at.b * T * D + at.c;
   const E* X = static_cast<const E*>(a.X) + base;
   const GT* G = static_cast<const GT*>(a.G) + base;
   E* H = static_cast<E*>(a.H) + base;
@@ -240,83 +318,79 @@ __global__ void __launch_bounds__(kThreads, CTAS)
   auto fetch = [&](unsigned p) {
     mark = load_reset<R, false>(a, at.b, p);
     if (!at.ok || p >= T) return;
-    const E* x = X + p * D;
-    const GT* g = G + p * D;
-    const int n = min(T - p, (unsigned)R);
+    const E* x = X + (size_t)p * D;
+    const GT* g = G + (size_t)p * D;
+    if (T - p >= R) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i < n) {
-        rx[i].load(x + i * D);
-        rg[i].load(g + i * D);
+      for (int i = 0; i < R; ++i) {
+        rx[i].load(rows(x, i, D));
+        rg[i].load(rows(g, i, D));
       }
+    } else {
+      const int n = T - p;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i < n) {
+          rx[i].load(rows(x, i, D));
+          rg[i].load(rows(g, i, D));
+        }
+    }
   };
   unsigned pos = ((unsigned)at.rank * kWarps + (threadIdx.x >> 5)) * R;
   const unsigned rounds = (T + stride - 1) / stride;
   fetch(pos);
-  cluster_sync(at.cl);
-  float carry[VC];
-  load_state(a.h0, a, at, carry);
+  join_init(js, at.cl);
+  V carry = load_state<VC>(a.h0, a, at);
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
-    float av[R][VC], u[R][VC];
+    V av[R], u[R];
     const int n = pos >= T ? 0 : (int)min(T - pos, (unsigned)R);
     const unsigned rs = __ballot_sync(~0u, mark != 0);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        const float x = rx[i].get(k), g = rg[i].get(k);
-        av[i][k] = g;
-        u[i][k] = x;
-        if constexpr (SIG) {
-          float na;
-          gate_of(g, av[i][k], na);
-          u[i][k] = na * x;
-        }
-        if (i >= n) av[i][k] = 1.f, u[i][k] = 0.f;
+    for (int i = 0; i < R; ++i) {
+      av[i] = rg[i].get();
+      u[i] = rx[i].get();
+      if constexpr (SIG) {
+        V na;
+        gate_of(av[i], av[i], na);
+        u[i] = mul(na, u[i]);
       }
-    fetch(pos + stride);
-    Map<VC> m;
+    }
+    if (n < R)
 #pragma unroll
-    for (int k = 0; k < VC; ++k) m.A[k] = 1.f, m.U[k] = 0.f;
+      for (int i = 0; i < R; ++i)
+        if (i >= n) av[i] = all<VC>(1.f), u[i] = all<VC>(0.f);
+    fetch(pos + stride);
+    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
     if (rs == 0) {
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          m.A[k] *= av[i][k];
-          m.U[k] = fmaf(av[i][k], m.U[k], u[i][k]);
-        }
+      for (int i = 0; i < R; ++i) {
+        m.A = mul(m.A, av[i]);
+        m.U = fma(av[i], m.U, u[i]);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int k = 0; k < VC; ++k)
-          m.U[k] = rs >> i & 1 ? u[i][k] : fmaf(av[i][k], m.U[k], u[i][k]);
+      for (int i = 0; i < R; ++i) m.U = pick(rs >> i & 1, u[i], fma(av[i], m.U, u[i]));
     }
-    float h[VC];
-    join_runs(js, round & 1, at.cl, at.rank, m, rs != 0, carry, h);
+    V h = join_runs(js, round, at.cl, at.rank, m, rs != 0, carry, a.err);
     if (at.ok) {
-      E* out = H + pos * D;
+      E* out = H + (size_t)pos * D;
       if (rs == 0 && n == R) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-#pragma unroll
-          for (int k = 0; k < VC; ++k) h[k] = fmaf(av[i][k], h[k], u[i][k]);
-          Raw<E, VC>::store(out + i * D, h);
+          h = fma(av[i], h, u[i]);
+          Raw<E, VC>::store(rows(out, i, D), h);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < R; ++i)
           if (i < n) {
-#pragma unroll
-            for (int k = 0; k < VC; ++k)
-              h[k] = rs >> i & 1 ? u[i][k] : fmaf(av[i][k], h[k], u[i][k]);
-            Raw<E, VC>::store(out + i * D, h);
+            h = pick(rs >> i & 1, u[i], fma(av[i], h, u[i]));
+            Raw<E, VC>::store(rows(out, i, D), h);
           }
       }
     }
   }
-  store_state(a.h_final, a, at, carry);
+  store_state<VC>(a.h_final, a, at, carry);
 }
 
 // ---------------------------------------------------------------------------------- backward
@@ -326,10 +400,11 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 template <typename E, typename GT, bool SIG, int VC, int R, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS)
     recur_bwd_kernel(const __grid_constant__ RecurArgs a, const int cluster) {
+  using V = Vec<VC>;
   __shared__ Joins<VC> js;
   const Place<VC> at(a, cluster);
-  const unsigned T = a.T, stride = (unsigned)at.cl * kWarps * R;
-  const size_t D = a.D, base = (size_t)at.b * T * D + at.c;
+  const unsigned T = a.T, D = a.D, stride = (unsigned)at.cl * kWarps * R;
+  const size_t base = (size_t)at.b * T * D + at.c;
   const E* X = static_cast<const E*>(a.X) + base;
   const GT* G = static_cast<const GT*>(a.G) + base;
   const E* H = static_cast<const E*>(a.H_in) + base;
@@ -343,80 +418,102 @@ __global__ void __launch_bounds__(kThreads, CTAS)
   auto fetch = [&](unsigned p) {
     mark = load_reset<R, true>(a, at.b, p);
     if (!at.ok || p >= T) return;
-    const size_t o = (T - 1 - p) * D;
+    const size_t o = (size_t)(T - 1 - p) * D;
     const int n = min(T - p, (unsigned)R), nh = min(T - 1 - p, (unsigned)R);
+    if (nh == R) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (i < n) {
-        rg[i].load(G + o - i * D);
-        rd[i].load(dH + o - i * D);
-        if constexpr (SIG) rx[i].load(X + o - i * D);
+      for (int i = 0; i < R; ++i) {
+        rg[i].load(rows_back(G + o, i, D));
+        rd[i].load(rows_back(dH + o, i, D));
+        if constexpr (SIG) rx[i].load(rows_back(X + o, i, D));
+        rh[i].load(rows_back(H + o, i + 1, D));
       }
-      if (i < nh) rh[i].load(H + o - (i + 1) * D);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (i < n) {
+          rg[i].load(rows_back(G + o, i, D));
+          rd[i].load(rows_back(dH + o, i, D));
+          if constexpr (SIG) rx[i].load(rows_back(X + o, i, D));
+        }
+        if (i < nh) rh[i].load(rows_back(H + o, i + 1, D));
+      }
     }
   };
   unsigned pos = ((unsigned)at.rank * kWarps + (threadIdx.x >> 5)) * R;
   const unsigned rounds = (T + stride - 1) / stride;
   fetch(pos);
-  cluster_sync(at.cl);
-  float carry[VC], h0[VC];
-  load_state(a.dh_final, a, at, carry);
-  load_state(a.h0, a, at, h0);
+  join_init(js, at.cl);
+  V carry = load_state<VC>(a.dh_final, a, at);
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
-    // dg: dG / (D) before the adjoint is known: h_{t-1}, or (h_{t-1} - x) a (1 - a)
-    float av[R][VC], na[SIG ? R : 1][VC], dg[R][VC];
-    Raw<E, VC> dh[R];
+    // dg: dG / D_t, which is h_{t-1}, or (h_{t-1} - x) a (1 - a)
+    V av[R], na[SIG ? R : 1], dg[R], dh[R];
     const int n = pos >= T ? 0 : (int)min(T - pos, (unsigned)R);
     const unsigned rs = __ballot_sync(~0u, mark != 0);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      dh[i] = rd[i];
+      dh[i] = rd[i].get();
+      av[i] = rg[i].get();
+      dg[i] = rh[i].get();
+    }
+    if (n > 0 && pos + n == T) {  // token 0 comes from h0
+      const V h0 = load_state<VC>(a.h0, a, at);
 #pragma unroll
-      for (int k = 0; k < VC; ++k) {
-        av[i][k] = rg[i].get(k);
-        float prev = pos + i == T - 1 ? h0[k] : rh[i].get(k);
-        if (rs >> i & 1) prev = 0.f;
-        dg[i][k] = prev;
-        if constexpr (SIG) {
-          gate_of(av[i][k], av[i][k], na[i][k]);
-          dg[i][k] = (prev - rx[i].get(k)) * (av[i][k] * na[i][k]);
-        }
+      for (int i = 0; i < R; ++i)
+        if (i == n - 1) dg[i] = h0;
+    }
+    if (rs)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (rs >> i & 1) dg[i] = all<VC>(0.f);
+    if constexpr (SIG) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        gate_of(av[i], av[i], na[i]);
+        dg[i] = mul(fma(rx[i].get(), all<VC>(-1.f), dg[i]), mul(av[i], na[i]));
       }
     }
     fetch(pos + stride);
-    Map<VC> m;
+    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
+    if (rs == 0 && n == R) {
 #pragma unroll
-    for (int k = 0; k < VC; ++k) m.A[k] = 1.f, m.U[k] = 0.f;
+      for (int i = 0; i < R; ++i) {
+        m.A = mul(m.A, av[i]);
+        m.U = mul(av[i], add(dh[i], m.U));
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i < n)
-#pragma unroll
-        for (int k = 0; k < VC; ++k) {
-          m.A[k] *= av[i][k];
-          m.U[k] = rs >> i & 1 ? 0.f : av[i][k] * (dh[i].get(k) + m.U[k]);
+      for (int i = 0; i < R; ++i)
+        if (i < n) {
+          m.A = mul(m.A, av[i]);
+          m.U = pick(rs >> i & 1, all<VC>(0.f), mul(av[i], add(dh[i], m.U)));
         }
-    float c[VC];
-    join_runs(js, round & 1, at.cl, at.rank, m, rs != 0, carry, c);
-    if (at.ok && n > 0) {
-      const size_t o = (T - 1 - pos) * D;
+    }
+    V c = join_runs(js, round, at.cl, at.rank, m, rs != 0, carry, a.err);
+    if (!at.ok || n == 0) continue;
+    const size_t o = (size_t)(T - 1 - pos) * D;
+    if (rs == 0 && n == R) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const V Dt = add(dh[i], c);
+        c = mul(av[i], Dt);
+        Raw<E, VC>::store(rows_back(dX + o, i, D), SIG ? mul(na[SIG ? i : 0], Dt) : Dt);
+        Raw<GT, VC>::store(rows_back(dG + o, i, D), mul(Dt, dg[i]));
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i < n) {
           const bool first = rs >> i & 1;
-          float x[VC], g[VC];
-#pragma unroll
-          for (int k = 0; k < VC; ++k) {
-            const float Dt = dh[i].get(k) + c[k];
-            x[k] = SIG ? na[SIG ? i : 0][k] * Dt : Dt;
-            g[k] = !SIG && first ? 0.f : Dt * dg[i][k];
-            c[k] = first ? 0.f : av[i][k] * Dt;
-          }
-          Raw<E, VC>::store(dX + o - i * D, x);
-          Raw<GT, VC>::store(dG + o - i * D, g);
+          const V Dt = add(dh[i], c);
+          c = pick(first, all<VC>(0.f), mul(av[i], Dt));
+          Raw<E, VC>::store(rows_back(dX + o, i, D), SIG ? mul(na[SIG ? i : 0], Dt) : Dt);
+          Raw<GT, VC>::store(rows_back(dG + o, i, D),
+                             pick(!SIG && first, all<VC>(0.f), mul(Dt, dg[i])));
         }
     }
   }
-  store_state(a.dh0, a, at, carry);
+  store_state<VC>(a.dh0, a, at, carry);
 }
 
 // -------------------------------------------------------------------------------------- step
@@ -436,27 +533,24 @@ __global__ void __launch_bounds__(kStepThreads) recur_step_kernel(const __grid_c
   float* st = a.state + (size_t)slot * a.D + c;
   Raw<E, VC> rx;
   Raw<GT, VC> rg;
-  float h[VC];
+  Vec<VC> h;
   auto fetch = [&](int row) {
     rx.load(static_cast<const E*>(a.X) + (size_t)row * a.D + c);
     rg.load(static_cast<const GT*>(a.G) + (size_t)row * a.D + c);
   };
   auto token = [&](int row) {
-#pragma unroll
-    for (int k = 0; k < VC; ++k) {
-      float aa = rg.get(k), u = rx.get(k), na;
-      if constexpr (SIG) {
-        gate_of(aa, aa, na);
-        u *= na;
-      }
-      h[k] = fmaf(aa, h[k], u);
+    Vec<VC> aa = rg.get(), u = rx.get(), na;
+    if constexpr (SIG) {
+      gate_of(aa, aa, na);
+      u = mul(u, na);
     }
+    h = fma(aa, h, u);
     Raw<E, VC>::store(static_cast<E*>(a.H) + (size_t)row * a.D + c, h);
   };
   if (ok) {
     fetch(b);
-#pragma unroll
-    for (int k = 0; k < VC; ++k) h[k] = st[k];
+    if constexpr (VC == 1) h = *st;
+    else h = *reinterpret_cast<const float2*>(st);
   }
   bool later = false;
   if (a.slots) {
@@ -517,24 +611,28 @@ cudaError_t launch(K kernel, const RecurArgs& a, int vc, int run, cudaStream_t s
 #define RB 8
 #define CF 3
 #define CB 2
+#define R1F 8
+#define C1F 3
+#define R1B 8
+#define C1B 2
 #endif
 cudaError_t recur_fwd(const RecurArgs& a, cudaStream_t s) {
   const bool two = a.bf16 && a.D % 2 == 0;
   if (two && a.sigmoid) return launch(recur_fwd_kernel<bf16, bf16, true, 2, RF, CF>, a, 2, RF, s);
   if (two) return launch(recur_fwd_kernel<bf16, float, false, 2, RF, CF>, a, 2, RF, s);
-  if (a.bf16 && a.sigmoid) return launch(recur_fwd_kernel<bf16, bf16, true, 1, 16, 3>, a, 1, 16, s);
-  if (a.bf16) return launch(recur_fwd_kernel<bf16, float, false, 1, 16, 3>, a, 1, 16, s);
-  if (a.sigmoid) return launch(recur_fwd_kernel<float, float, true, 1, 16, 3>, a, 1, 16, s);
-  return launch(recur_fwd_kernel<float, float, false, 1, 16, 3>, a, 1, 16, s);
+  if (a.bf16 && a.sigmoid) return launch(recur_fwd_kernel<bf16, bf16, true, 1, R1F, C1F>, a, 1, R1F, s);
+  if (a.bf16) return launch(recur_fwd_kernel<bf16, float, false, 1, R1F, C1F>, a, 1, R1F, s);
+  if (a.sigmoid) return launch(recur_fwd_kernel<float, float, true, 1, R1F, C1F>, a, 1, R1F, s);
+  return launch(recur_fwd_kernel<float, float, false, 1, R1F, C1F>, a, 1, R1F, s);
 }
 cudaError_t recur_bwd(const RecurArgs& a, cudaStream_t s) {
   const bool two = a.bf16 && a.D % 2 == 0;
   if (two && a.sigmoid) return launch(recur_bwd_kernel<bf16, bf16, true, 2, RB, CB>, a, 2, RB, s);
   if (two) return launch(recur_bwd_kernel<bf16, float, false, 2, RB, CB>, a, 2, RB, s);
-  if (a.bf16 && a.sigmoid) return launch(recur_bwd_kernel<bf16, bf16, true, 1, 8, 2>, a, 1, 8, s);
-  if (a.bf16) return launch(recur_bwd_kernel<bf16, float, false, 1, 8, 2>, a, 1, 8, s);
-  if (a.sigmoid) return launch(recur_bwd_kernel<float, float, true, 1, 8, 2>, a, 1, 8, s);
-  return launch(recur_bwd_kernel<float, float, false, 1, 8, 2>, a, 1, 8, s);
+  if (a.bf16 && a.sigmoid) return launch(recur_bwd_kernel<bf16, bf16, true, 1, R1B, C1B>, a, 1, R1B, s);
+  if (a.bf16) return launch(recur_bwd_kernel<bf16, float, false, 1, R1B, C1B>, a, 1, R1B, s);
+  if (a.sigmoid) return launch(recur_bwd_kernel<float, float, true, 1, R1B, C1B>, a, 1, R1B, s);
+  return launch(recur_bwd_kernel<float, float, false, 1, R1B, C1B>, a, 1, R1B, s);
 }
 cudaError_t recur_step(const RecurArgs& a, cudaStream_t s) {
   const int vc = a.D % 2 == 0 ? 2 : 1;

@@ -29,7 +29,6 @@ namespace tttk {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int kSMs = 148;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
 
@@ -57,11 +56,10 @@ __device__ __forceinline__ V pick(bool c, V a, V b) {
   else return make_float2(c ? a.x : b.x, c ? a.y : b.y);
 }
 
-// a = sigmoid(g) = 1 / (1 + e) and 1 - a = e a with e = exp(-g): neither is a difference. e is
-// held at 2^126, where a is the smallest normal number and 1 - a is 1; a NaN stays one.
-__device__ __forceinline__ float exp2_held(float x) {
+// a = sigmoid(g) = 1 / (1 + e) and 1 - a = e a with e = exp(-g): neither is a difference. Logits
+// come held at -87 (Raw::hold), where a is 2e-38 and 1 - a is 1: beyond, e would overflow.
+__device__ __forceinline__ float exp2_of(float x) {
   float e;
-  asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(x) : "f"(x));  // 126
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
   return e;
 }
@@ -72,19 +70,20 @@ __device__ __forceinline__ float recip(float x) {
 }
 constexpr float kNegLog2e = -1.44269504f;
 __device__ __forceinline__ void gate_of(float g, float& a, float& na) {
-  const float e = exp2_held(g * kNegLog2e);
+  const float e = exp2_of(g * kNegLog2e);
   a = recip(1.f + e);
   na = e * a;
 }
 __device__ __forceinline__ void gate_of(float2 g, float2& a, float2& na) {
   const float2 x = mul2(g, both(kNegLog2e));
-  const float2 e = make_float2(exp2_held(x.x), exp2_held(x.y));
+  const float2 e = make_float2(exp2_of(x.x), exp2_of(x.y));
   const float2 q = add2(e, both(1.f));
   a = make_float2(recip(q.x), recip(q.y));
   na = mul2(e, a);
 }
 
-// VC neighbouring elements of a row as they lie in memory.
+// VC neighbouring elements of a row as they lie in memory. hold: at least -87 (0xC2AE in bf16); a
+// NaN stays one.
 template <typename E, int VC>
 struct Raw;
 template <>
@@ -93,6 +92,7 @@ struct Raw<bf16, 1> {
   __device__ __forceinline__ void load(const bf16* p) {
     asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
   }
+  __device__ __forceinline__ void hold() { asm("max.NaN.bf16 %0, %0, %1;" : "+h"(r) : "h"((unsigned short)0xC2AE)); }
   __device__ __forceinline__ float get() const { return __uint_as_float((uint32_t)r << 16); }
   static __device__ __forceinline__ void store(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
@@ -102,6 +102,7 @@ struct Raw<bf16, 2> {
   __device__ __forceinline__ void load(const bf16* p) {
     asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r) : "l"(p));
   }
+  __device__ __forceinline__ void hold() { asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(0xC2AEC2AEu)); }
   __device__ __forceinline__ float2 get() const { return make_float2(bf16lo(r), bf16hi(r)); }
   static __device__ __forceinline__ void store(bf16* p, float2 v) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
@@ -113,6 +114,7 @@ struct Raw<float, 1> {
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.L1::no_allocate.f32 %0, [%1];" : "=f"(r) : "l"(p));
   }
+  __device__ __forceinline__ void hold() { asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(r)); }
   __device__ __forceinline__ float get() const { return r; }
   static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 };
@@ -121,6 +123,10 @@ struct Raw<float, 2> {
   float2 r;
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.L1::no_allocate.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  }
+  __device__ __forceinline__ void hold() {
+    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(r.x));
+    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(r.y));
   }
   __device__ __forceinline__ float2 get() const { return r; }
   static __device__ __forceinline__ void store(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
@@ -205,19 +211,18 @@ __device__ __forceinline__ void join_init(Joins<VC>& js, int cl) {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// h through maps 0..n-1 in order; `in` is h before map `mine`. resets: bit s for map s.
-template <int VC, int N>
-__device__ __forceinline__ void fold(const Map<VC> (*maps)[32], int n, unsigned resets, int mine,
-                                     Vec<VC>& h, Vec<VC>& in) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int s = 0; s < N; ++s)
-    if (s < n) {
-      const Map<VC> q = maps[s][lane];
-      if (s == mine) in = h;
-      h = fma(q.A, h, q.U);
-      if (resets >> s & 1) h = q.U;
-    }
+// h through maps lo..hi-1 in order (lo and hi uniform over the warp). resets: bit s for map s.
+template <int VC>
+__device__ __forceinline__ Vec<VC> fold(const Map<VC> (*maps)[32], int lo, int hi, unsigned resets,
+                                        Vec<VC> h) {
+  const Map<VC>* m = &maps[0][threadIdx.x & 31];
+  if (resets == 0) {
+#pragma unroll 2
+    for (int s = lo; s < hi; ++s) h = fma(m[s * 32].A, h, m[s * 32].U);
+  } else {
+    for (int s = lo; s < hi; ++s) h = pick(resets >> s & 1, m[s * 32].U, fma(m[s * 32].A, h, m[s * 32].U));
+  }
+  return h;
 }
 
 // Joins the warps' maps m (reset: it holds a document's first token) of one round: `carry` goes
@@ -237,43 +242,38 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
   if (cl > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(full, cl * (32 * sizeof(Map<VC>) + 4));
   __syncthreads();
   const unsigned rs = __ballot_sync(~0u, lane < kWarps && js.seg_reset[buf][lane & (kWarps - 1)]);
-  Vec<VC> h = carry, in = carry;
-  if (cl > 1) {
-    if (w < cl) {  // warp w hands the CTA's map to CTA w
-      Map<VC> c{all<VC>(1.f), all<VC>(0.f)};
-#pragma unroll
-      for (int s = 0; s < kWarps; ++s) {
-        const Map<VC> q = js.seg[buf][s][lane];
-        c.A = mul(c.A, q.A);
-        c.U = fma(q.A, c.U, q.U);
-        if (rs >> s & 1) c.U = q.U;
-      }
-      const uint32_t bar = remote(full, w);
-      st_async(remote(smem_u32(&js.cta[buf][rank][lane]), w), c, bar);
-      if (lane == 0) st_async(remote(smem_u32(&js.cta_reset[buf][rank]), w), rs, bar);
-    }
-    wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
-    const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][lane & (kMaxCluster - 1)]);
-    fold<VC, kMaxCluster>(js.cta[buf], cl, crs, rank, h, in);
-    carry = h;
-    h = in;
+  if (cl == 1) {
+    const Vec<VC> in = fold<VC>(js.seg[buf], 0, w, rs, carry);
+    carry = fold<VC>(js.seg[buf], w, kWarps, rs, in);
+    return in;
   }
-  fold<VC, kWarps>(js.seg[buf], kWarps, rs, w, h, in);
-  if (cl == 1) carry = h;
-  return in;
+  if (w < cl) {  // warp w hands the CTA's map to CTA w
+    Map<VC> c{all<VC>(1.f), fold<VC>(js.seg[buf], 0, kWarps, rs, all<VC>(0.f))};
+#pragma unroll 2
+    for (int s = 0; s < kWarps; ++s) c.A = mul(c.A, js.seg[buf][s][lane].A);
+    const uint32_t bar = remote(full, w);
+    st_async(remote(smem_u32(&js.cta[buf][rank][lane]), w), c, bar);
+    if (lane == 0) st_async(remote(smem_u32(&js.cta_reset[buf][rank]), w), rs, bar);
+  }
+  wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
+  const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][lane & (kMaxCluster - 1)]);
+  const Vec<VC> in = fold<VC>(js.cta[buf], 0, rank, crs, carry);
+  carry = fold<VC>(js.cta[buf], rank, cl, crs, in);
+  return fold<VC>(js.seg[buf], 0, w, rs, in);
 }
 
 // This thread's place: features c.. of batch row b, run w of CTA `rank` of the cluster.
 template <int VC>
 struct Place {
-  int b, c, cl, rank;
+  int b, c0, c, cl, rank;
   bool ok;
   __device__ __forceinline__ Place(const RecurArgs& a, int cluster) {
     cl = cluster;
     rank = cl > 1 ? (int)cluster_rank() : 0;
     const int blocks = (a.D + 32 * VC - 1) / (32 * VC), i = blockIdx.x / cl;
     b = i / blocks;
-    c = (i - b * blocks) * 32 * VC + (threadIdx.x & 31) * VC;
+    c0 = (i - b * blocks) * 32 * VC;
+    c = c0 + (threadIdx.x & 31) * VC;
     ok = c < a.D;
   }
 };
@@ -300,68 +300,132 @@ __device__ __forceinline__ unsigned load_reset(const RecurArgs& a, int b, unsign
   return a.reset[(size_t)b * a.T + (REV ? a.T - 1 - p : p)];
 }
 
+// --------------------------------------------------------------------------------- row loads
+// A warp's R rows of 32 VC elements in shared memory, filled ahead by asynchronous copies of CB
+// bytes (16 where the rows' starts allow it; 2: plain loads, no such copy exists).
+template <typename E, int VC, int R, int CB>
+struct RowTile {
+  static constexpr int kRow = 32 * VC * (int)sizeof(E), kBytes = R * kRow;
+  // Rows row0, row0 +- D, ...: n of them; `width` elements of each are the tensor's.
+  template <bool REV>
+  static __device__ __forceinline__ void fetch(uint32_t dst, const E* row0, unsigned D, int n,
+                                               int width) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (CB == 2 || (CB == 4 && kRow == 256)) {
+      // one thread, its own VC elements: the pair's two copies, or the plain 2-byte load
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const E* src = (REV ? rows_back(row0, i, D) : rows(row0, i, D)) + lane * VC;
+        const uint32_t to = dst + i * kRow + lane * VC * (int)sizeof(E);
+        if (i < n && lane * VC < width) {
+          if constexpr (CB == 2) {
+            const unsigned short v = *reinterpret_cast<const unsigned short*>(src);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
+          } else {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(src) : "memory");
+          }
+        }
+      }
+    } else {
+      constexpr int kLanes = kRow / CB, kStep = 32 / kLanes;
+      static_assert(kLanes <= 32 && R % kStep == 0, "whole rows per copy");
+      const int r0 = lane / kLanes, col = (lane % kLanes) * CB;
+      const bool in = col < width * (int)sizeof(E);
+      const E* src = (REV ? row0 - (size_t)r0 * D : row0 + (size_t)r0 * D) + col / (int)sizeof(E);
+      const uint32_t to = dst + r0 * kRow + col;
+#pragma unroll
+      for (int i = 0; i < R; i += kStep) {
+        const E* p = REV ? rows_back(src, i, D) : rows(src, i, D);
+        if (in && i + r0 < n) {
+          if constexpr (CB == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * kRow), "l"(p) : "memory");
+          else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + i * kRow), "l"(p) : "memory");
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ Raw<E, VC> get(const uint8_t* tile, int i) {
+    return *reinterpret_cast<const Raw<E, VC>*>(tile + i * kRow + (threadIdx.x & 31) * VC * (int)sizeof(E));
+  }
+};
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+constexpr int kStages = 3;  // rounds in shared memory: the one at hand and two on their way
+
 // ----------------------------------------------------------------------------------- forward
-template <typename E, typename GT, bool SIG, int VC, int R, int CTAS>
-__global__ void __launch_bounds__(kThreads, CTAS)
+template <typename E, typename GT, int VC, int R, int CB>
+struct FwdTiles {
+  using X = RowTile<E, VC, R, CB>;
+  using G = RowTile<GT, VC, R, sizeof(GT) == 4 && CB < 4 ? 4 : CB>;
+  static constexpr int kStage = X::kBytes + G::kBytes;  // of one warp
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+};
+template <typename E, typename GT, bool SIG, int VC, int R, int CB>
+__global__ void __launch_bounds__(kThreads, 2)
     recur_fwd_kernel(const __grid_constant__ RecurArgs a, const int cluster) {
   using V = Vec<VC>;
+  using Tl = FwdTiles<E, GT, VC, R, CB>;
+  extern __shared__ __align__(16) uint8_t tiles[];
   __shared__ Joins<VC> js;
   const Place<VC> at(a, cluster);
   const unsigned T = a.T, D = a.D, stride = (unsigned)at.cl * kWarps * R;
-  const size_t base = (size_t)at.b * T * D + at.c;
+  const int w = threadIdx.x >> 5;
+  uint8_t* mine = tiles + w * kStages * Tl::kStage;
+  const size_t base = (size_t)at.b * T * D + at.c0;
   const E* X = static_cast<const E*>(a.X) + base;
   const GT* G = static_cast<const GT*>(a.G) + base;
-  E* H = static_cast<E*>(a.H) + base;
-  Raw<E, VC> rx[R];
-  Raw<GT, VC> rg[R];
-  unsigned mark;
-  auto fetch = [&](unsigned p) {
-    mark = load_reset<R, false>(a, at.b, p);
-    if (!at.ok || p >= T) return;
-    const E* x = X + (size_t)p * D;
-    const GT* g = G + (size_t)p * D;
-    if (T - p >= R) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        rx[i].load(rows(x, i, D));
-        rg[i].load(rows(g, i, D));
-      }
-    } else {
-      const int n = T - p;
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (i < n) {
-          rx[i].load(rows(x, i, D));
-          rg[i].load(rows(g, i, D));
-        }
+  E* H = static_cast<E*>(a.H) + base + (at.c - at.c0);
+  unsigned mark[kStages - 1];
+  auto fetch = [&](unsigned p, int st) {
+    if (p < T) {
+      const int n = min(T - p, (unsigned)R);
+      const uint32_t dst = smem_u32(mine) + st * Tl::kStage;
+      Tl::X::template fetch<false>(dst, X + (size_t)p * D, D, n, a.D - at.c0);
+      Tl::G::template fetch<false>(dst + Tl::X::kBytes, G + (size_t)p * D, D, n, a.D - at.c0);
     }
+    cp_commit();
   };
-  unsigned pos = ((unsigned)at.rank * kWarps + (threadIdx.x >> 5)) * R;
+  unsigned pos = ((unsigned)at.rank * kWarps + w) * R;
   const unsigned rounds = (T + stride - 1) / stride;
-  fetch(pos);
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) {
+    fetch(pos + k * stride, k);
+    mark[k] = load_reset<R, false>(a, at.b, pos + k * stride);
+  }
   join_init(js, at.cl);
   V carry = load_state<VC>(a.h0, a, at);
+  int st = 0, ahead = kStages - 1;
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
     V av[R], u[R];
     const int n = pos >= T ? 0 : (int)min(T - pos, (unsigned)R);
-    const unsigned rs = __ballot_sync(~0u, mark != 0);
+    const unsigned rs = __ballot_sync(~0u, mark[0] != 0);
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) mark[k] = mark[k + 1];
+    mark[kStages - 2] = load_reset<R, false>(a, at.b, pos + (kStages - 1) * stride);
+    fetch(pos + (kStages - 1) * stride, ahead);
+    cp_wait<kStages - 1>();
+    __syncwarp();
+    const uint8_t* tile = mine + st * Tl::kStage;
+    if (++st == kStages) st = 0;
+    if (++ahead == kStages) ahead = 0;
+    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      av[i] = rg[i].get();
-      u[i] = rx[i].get();
+      u[i] = Tl::X::get(tile, i).get();
+      Raw<GT, VC> g = Tl::G::get(tile + Tl::X::kBytes, i);
       if constexpr (SIG) {
+        g.hold();
         V na;
-        gate_of(av[i], av[i], na);
+        gate_of(g.get(), av[i], na);
         u[i] = mul(na, u[i]);
+      } else {
+        av[i] = g.get();
       }
     }
-    if (n < R)
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (i >= n) av[i] = all<VC>(1.f), u[i] = all<VC>(0.f);
-    fetch(pos + stride);
-    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
-    if (rs == 0) {
+    __syncwarp();  // the stage may be filled again
+    if (rs == 0 && n == R) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         m.A = mul(m.A, av[i]);
@@ -369,25 +433,28 @@ __global__ void __launch_bounds__(kThreads, CTAS)
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < R; ++i) m.U = pick(rs >> i & 1, u[i], fma(av[i], m.U, u[i]));
+      for (int i = 0; i < R; ++i)
+        if (i < n) {
+          m.A = mul(m.A, av[i]);
+          m.U = pick(rs >> i & 1, u[i], fma(av[i], m.U, u[i]));
+        }
     }
     V h = join_runs(js, round, at.cl, at.rank, m, rs != 0, carry, a.err);
-    if (at.ok) {
-      E* out = H + (size_t)pos * D;
-      if (rs == 0 && n == R) {
+    if (!at.ok) continue;
+    E* out = H + (size_t)pos * D;
+    if (rs == 0 && n == R) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          h = fma(av[i], h, u[i]);
+      for (int i = 0; i < R; ++i) {
+        h = fma(av[i], h, u[i]);
+        Raw<E, VC>::store(rows(out, i, D), h);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i < n) {
+          h = pick(rs >> i & 1, u[i], fma(av[i], h, u[i]));
           Raw<E, VC>::store(rows(out, i, D), h);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (i < n) {
-            h = pick(rs >> i & 1, u[i], fma(av[i], h, u[i]));
-            Raw<E, VC>::store(rows(out, i, D), h);
-          }
-      }
     }
   }
   store_state<VC>(a.h_final, a, at, carry);
@@ -396,120 +463,131 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 // ---------------------------------------------------------------------------------- backward
 // The adjoint runs backwards over the tokens: with c the part of D_{t-1} that comes from token t,
 //   D_t = dH_t + c_{t+1},  c_t = a_t D_t  (0 at a document's first token),
-// a recurrence in c of the same form, walked from the last token.
-template <typename E, typename GT, bool SIG, int VC, int R, int CTAS>
-__global__ void __launch_bounds__(kThreads, CTAS)
+// a recurrence in c of the same form, walked from the last token. The decays stay in registers
+// between the two passes over a run; the other inputs are read from shared memory again.
+template <typename E, typename GT, bool SIG, int VC, int R, int CB>
+struct BwdTiles {
+  using X = RowTile<E, VC, R, CB>;
+  using G = RowTile<GT, VC, R, sizeof(GT) == 4 && CB < 4 ? 4 : CB>;
+  static constexpr int oD = G::kBytes, oH = oD + X::kBytes, oX = oH + X::kBytes;
+  static constexpr int kStage = oX + (SIG ? X::kBytes : 0);  // of one warp
+  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+};
+template <typename E, typename GT, bool SIG, int VC, int R, int CB>
+__global__ void __launch_bounds__(kThreads, 2)
     recur_bwd_kernel(const __grid_constant__ RecurArgs a, const int cluster) {
   using V = Vec<VC>;
+  using Tl = BwdTiles<E, GT, SIG, VC, R, CB>;
+  extern __shared__ __align__(16) uint8_t tiles[];
   __shared__ Joins<VC> js;
   const Place<VC> at(a, cluster);
   const unsigned T = a.T, D = a.D, stride = (unsigned)at.cl * kWarps * R;
-  const size_t base = (size_t)at.b * T * D + at.c;
+  const int w = threadIdx.x >> 5;
+  uint8_t* mine = tiles + w * kStages * Tl::kStage;
+  const size_t base = (size_t)at.b * T * D + at.c0;
   const E* X = static_cast<const E*>(a.X) + base;
   const GT* G = static_cast<const GT*>(a.G) + base;
   const E* H = static_cast<const E*>(a.H_in) + base;
   const E* dH = static_cast<const E*>(a.dH) + base;
-  E* dX = static_cast<E*>(a.dX) + base;
-  GT* dG = static_cast<GT*>(a.dG) + base;
-  Raw<E, VC> rd[R], rx[SIG ? R : 1], rh[R];
-  Raw<GT, VC> rg[R];
-  unsigned mark;
-  // position p is token T - 1 - p; rh holds the state before the token, row T - 2 - p
-  auto fetch = [&](unsigned p) {
-    mark = load_reset<R, true>(a, at.b, p);
-    if (!at.ok || p >= T) return;
-    const size_t o = (size_t)(T - 1 - p) * D;
-    const int n = min(T - p, (unsigned)R), nh = min(T - 1 - p, (unsigned)R);
-    if (nh == R) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        rg[i].load(rows_back(G + o, i, D));
-        rd[i].load(rows_back(dH + o, i, D));
-        if constexpr (SIG) rx[i].load(rows_back(X + o, i, D));
-        rh[i].load(rows_back(H + o, i + 1, D));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (i < n) {
-          rg[i].load(rows_back(G + o, i, D));
-          rd[i].load(rows_back(dH + o, i, D));
-          if constexpr (SIG) rx[i].load(rows_back(X + o, i, D));
-        }
-        if (i < nh) rh[i].load(rows_back(H + o, i + 1, D));
-      }
+  E* dX = static_cast<E*>(a.dX) + base + (at.c - at.c0);
+  GT* dG = static_cast<GT*>(a.dG) + base + (at.c - at.c0);
+  unsigned mark[kStages - 1];
+  // position p is token T - 1 - p; the H tile holds the states before the tokens, from row T - 2 - p
+  auto fetch = [&](unsigned p, int st) {
+    if (p < T) {
+      const int n = min(T - p, (unsigned)R), nh = min(T - 1 - p, (unsigned)R), width = a.D - at.c0;
+      const uint32_t dst = smem_u32(mine) + st * Tl::kStage;
+      const size_t o = (size_t)(T - 1 - p) * D;
+      Tl::G::template fetch<true>(dst, G + o, D, n, width);
+      Tl::X::template fetch<true>(dst + Tl::oD, dH + o, D, n, width);
+      if (nh > 0) Tl::X::template fetch<true>(dst + Tl::oH, H + o - D, D, nh, width);
+      if constexpr (SIG) Tl::X::template fetch<true>(dst + Tl::oX, X + o, D, n, width);
     }
+    cp_commit();
   };
-  unsigned pos = ((unsigned)at.rank * kWarps + (threadIdx.x >> 5)) * R;
+  unsigned pos = ((unsigned)at.rank * kWarps + w) * R;
   const unsigned rounds = (T + stride - 1) / stride;
-  fetch(pos);
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) {
+    fetch(pos + k * stride, k);
+    mark[k] = load_reset<R, true>(a, at.b, pos + k * stride);
+  }
   join_init(js, at.cl);
   V carry = load_state<VC>(a.dh_final, a, at);
+  int st = 0, ahead = kStages - 1;
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
-    // dg: dG / D_t, which is h_{t-1}, or (h_{t-1} - x) a (1 - a)
-    V av[R], na[SIG ? R : 1], dg[R], dh[R];
+    V av[R], na[SIG ? R : 1];
     const int n = pos >= T ? 0 : (int)min(T - pos, (unsigned)R);
-    const unsigned rs = __ballot_sync(~0u, mark != 0);
+    const unsigned rs = __ballot_sync(~0u, mark[0] != 0);
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) mark[k] = mark[k + 1];
+    mark[kStages - 2] = load_reset<R, true>(a, at.b, pos + (kStages - 1) * stride);
+    __syncwarp();  // all lanes have left the last round's tile, which is filled next
+    fetch(pos + (kStages - 1) * stride, ahead);
+    cp_wait<kStages - 1>();
+    __syncwarp();
+    const uint8_t* tile = mine + st * Tl::kStage;
+    if (++st == kStages) st = 0;
+    if (++ahead == kStages) ahead = 0;
+    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      dh[i] = rd[i].get();
-      av[i] = rg[i].get();
-      dg[i] = rh[i].get();
-    }
-    if (n > 0 && pos + n == T) {  // token 0 comes from h0
-      const V h0 = load_state<VC>(a.h0, a, at);
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (i == n - 1) dg[i] = h0;
-    }
-    if (rs)
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (rs >> i & 1) dg[i] = all<VC>(0.f);
-    if constexpr (SIG) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        gate_of(av[i], av[i], na[i]);
-        dg[i] = mul(fma(rx[i].get(), all<VC>(-1.f), dg[i]), mul(av[i], na[i]));
+      Raw<GT, VC> g = Tl::G::get(tile, i);
+      if constexpr (SIG) {
+        g.hold();
+        gate_of(g.get(), av[i], na[i]);
+      } else {
+        av[i] = g.get();
       }
     }
-    fetch(pos + stride);
-    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
-    if (rs == 0 && n == R) {
+    const bool plain = rs == 0 && n == R && pos + R < T;
+    if (plain) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         m.A = mul(m.A, av[i]);
-        m.U = mul(av[i], add(dh[i], m.U));
+        m.U = mul(av[i], add(Tl::X::get(tile + Tl::oD, i).get(), m.U));
       }
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i < n) {
           m.A = mul(m.A, av[i]);
-          m.U = pick(rs >> i & 1, all<VC>(0.f), mul(av[i], add(dh[i], m.U)));
+          m.U = pick(rs >> i & 1, all<VC>(0.f),
+                     mul(av[i], add(Tl::X::get(tile + Tl::oD, i).get(), m.U)));
         }
     }
     V c = join_runs(js, round, at.cl, at.rank, m, rs != 0, carry, a.err);
     if (!at.ok || n == 0) continue;
     const size_t o = (size_t)(T - 1 - pos) * D;
-    if (rs == 0 && n == R) {
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const V Dt = add(dh[i], c);
-        c = mul(av[i], Dt);
-        Raw<E, VC>::store(rows_back(dX + o, i, D), SIG ? mul(na[SIG ? i : 0], Dt) : Dt);
-        Raw<GT, VC>::store(rows_back(dG + o, i, D), mul(Dt, dg[i]));
+    auto token = [&](int i, V prev, bool first) {
+      const V Dt = add(Tl::X::get(tile + Tl::oD, i).get(), c);
+      c = mul(av[i], Dt);
+      V x = Dt, g;
+      if constexpr (SIG) {
+        x = mul(na[i], Dt);
+        // D_t (h_{t-1} - x) a (1 - a)
+        g = mul(mul(c, na[i]), fma(Tl::X::get(tile + Tl::oX, i).get(), all<VC>(-1.f), prev));
+      } else {
+        g = first ? all<VC>(0.f) : mul(Dt, prev);
       }
+      if (first) c = all<VC>(0.f);
+      Raw<E, VC>::store(rows_back(dX + o, i, D), x);
+      Raw<GT, VC>::store(rows_back(dG + o, i, D), g);
+    };
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) token(i, Tl::X::get(tile + Tl::oH, i).get(), false);
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i < n) {
           const bool first = rs >> i & 1;
-          const V Dt = add(dh[i], c);
-          c = pick(first, all<VC>(0.f), mul(av[i], Dt));
-          Raw<E, VC>::store(rows_back(dX + o, i, D), SIG ? mul(na[SIG ? i : 0], Dt) : Dt);
-          Raw<GT, VC>::store(rows_back(dG + o, i, D),
-                             pick(!SIG && first, all<VC>(0.f), mul(Dt, dg[i])));
+          V prev = all<VC>(0.f);
+          if (!first) {
+            if (pos + i == T - 1) prev = load_state<VC>(a.h0, a, at);
+            else prev = Tl::X::get(tile + Tl::oH, i).get();
+          }
+          token(i, prev, first);
         }
     }
   }
@@ -539,6 +617,7 @@ __global__ void __launch_bounds__(kStepThreads) recur_step_kernel(const __grid_c
     rg.load(static_cast<const GT*>(a.G) + (size_t)row * a.D + c);
   };
   auto token = [&](int row) {
+    if constexpr (SIG) rg.hold();
     Vec<VC> aa = rg.get(), u = rx.get(), na;
     if constexpr (SIG) {
       gate_of(aa, aa, na);
@@ -575,22 +654,33 @@ __global__ void __launch_bounds__(kStepThreads) recur_step_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------------------------ launch
-// CTAs along the sequence: as few as bring the grid to two CTAs per SM, and no more than have a
-// run each.
-int cluster_of(const RecurArgs& a, int vc, int run) {
-  const long long ctas = (long long)a.B * ((a.D + 32 * vc - 1) / (32 * vc));
-  int cl = 1;
-  while (cl < kMaxCluster && ctas * cl < 2 * kSMs && (long long)cl * kWarps * run < a.T) cl *= 2;
-  return cl;
+// CTAs along the sequence. A cluster lies within one GPC, so that fewer CTAs than two per SM are
+// resident with the larger sizes (kResident, measured with the occupancy query). The choice is
+// the smallest count of rounds over all waves of the grid, with two rounds more per wave for its
+// start and end.
+int cluster_of(const RecurArgs& a, long long ctas, int run) {
+  constexpr int kResident[kMaxCluster + 1] = {0, 296, 296, 279, 284, 280, 270, 259, 264};
+  int best = 1;
+  long long least = 0;
+  for (int cl = 1; cl <= kMaxCluster; ++cl) {
+    if (cl > 1 && (long long)(cl - 1) * kWarps * run >= a.T) break;  // CTAs without a token
+    const long long waves = (ctas * cl + kResident[cl] - 1) / kResident[cl];
+    const long long tile = (long long)cl * kWarps * run, cost = waves * ((a.T + tile - 1) / tile + 2);
+    if (cl == 1 || cost < least) best = cl, least = cost;
+  }
+  return best;
 }
 template <typename K>
-cudaError_t launch(K kernel, const RecurArgs& a, int vc, int run, cudaStream_t s) {
-  const int cl = cluster_of(a, vc, run);
-  const long long ctas = (long long)a.B * ((a.D + 32 * vc - 1) / (32 * vc)) * cl;
-  if (ctas >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+cudaError_t launch(K kernel, size_t smem, const RecurArgs& a, int vc, int run, cudaStream_t s) {
+  const long long blocks = (long long)a.B * ((a.D + 32 * vc - 1) / (32 * vc));
+  const int cl = cluster_of(a, blocks, run);
+  if (blocks * cl >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = dim3((unsigned)(blocks * cl));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -599,41 +689,50 @@ cudaError_t launch(K kernel, const RecurArgs& a, int vc, int run, cudaStream_t s
   cfg.attrs = &at;
   cfg.numAttrs = cl > 1;
   count_launches(1);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, cl);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, cl);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+#ifndef RF
+#define RF 16
+#define RB 8
+#define R1F 16
+#define R1B 8
+#endif
+template <typename E, typename GT, bool SIG, int VC, int CB>
+cudaError_t fwd(const RecurArgs& a, cudaStream_t s) {
+  constexpr int R = sizeof(GT) * VC == 8 ? RF / 2 : VC == 2 ? RF : R1F;
+  return launch(recur_fwd_kernel<E, GT, SIG, VC, R, CB>, FwdTiles<E, GT, VC, R, CB>::kSmem, a, VC, R, s);
+}
+template <typename E, typename GT, bool SIG, int VC, int CB>
+cudaError_t bwd(const RecurArgs& a, cudaStream_t s) {
+  constexpr int R = VC == 2 ? RB : R1B;
+  return launch(recur_bwd_kernel<E, GT, SIG, VC, R, CB>, BwdTiles<E, GT, SIG, VC, R, CB>::kSmem, a, VC, R, s);
 }
 
 }  // namespace
 
-// Two features a thread where rows start on a pair's boundary and pairs are 32 bits (bf16 X).
-#ifndef RF
-#define RF 8
-#define RB 8
-#define CF 3
-#define CB 2
-#define R1F 8
-#define C1F 3
-#define R1B 8
-#define C1B 2
-#endif
-cudaError_t recur_fwd(const RecurArgs& a, cudaStream_t s) {
-  const bool two = a.bf16 && a.D % 2 == 0;
-  if (two && a.sigmoid) return launch(recur_fwd_kernel<bf16, bf16, true, 2, RF, CF>, a, 2, RF, s);
-  if (two) return launch(recur_fwd_kernel<bf16, float, false, 2, RF, CF>, a, 2, RF, s);
-  if (a.bf16 && a.sigmoid) return launch(recur_fwd_kernel<bf16, bf16, true, 1, R1F, C1F>, a, 1, R1F, s);
-  if (a.bf16) return launch(recur_fwd_kernel<bf16, float, false, 1, R1F, C1F>, a, 1, R1F, s);
-  if (a.sigmoid) return launch(recur_fwd_kernel<float, float, true, 1, R1F, C1F>, a, 1, R1F, s);
-  return launch(recur_fwd_kernel<float, float, false, 1, R1F, C1F>, a, 1, R1F, s);
-}
-cudaError_t recur_bwd(const RecurArgs& a, cudaStream_t s) {
-  const bool two = a.bf16 && a.D % 2 == 0;
-  if (two && a.sigmoid) return launch(recur_bwd_kernel<bf16, bf16, true, 2, RB, CB>, a, 2, RB, s);
-  if (two) return launch(recur_bwd_kernel<bf16, float, false, 2, RB, CB>, a, 2, RB, s);
-  if (a.bf16 && a.sigmoid) return launch(recur_bwd_kernel<bf16, bf16, true, 1, R1B, C1B>, a, 1, R1B, s);
-  if (a.bf16) return launch(recur_bwd_kernel<bf16, float, false, 1, R1B, C1B>, a, 1, R1B, s);
-  if (a.sigmoid) return launch(recur_bwd_kernel<float, float, true, 1, R1B, C1B>, a, 1, R1B, s);
-  return launch(recur_bwd_kernel<float, float, false, 1, R1B, C1B>, a, 1, R1B, s);
-}
+// bf16 takes two features a thread where rows start on a pair's boundary; copies are of 16 bytes
+// where rows do.
+#define RECUR_DISPATCH(f)                                                       \
+  do {                                                                          \
+    if (a.bf16 && a.sigmoid)                                                    \
+      return a.D % 8 == 0   ? f<bf16, bf16, true, 2, 16>(a, s)                  \
+             : a.D % 2 == 0 ? f<bf16, bf16, true, 2, 4>(a, s)                   \
+                            : f<bf16, bf16, true, 1, 2>(a, s);                  \
+    if (a.bf16)                                                                 \
+      return a.D % 8 == 0   ? f<bf16, float, false, 2, 16>(a, s)                \
+             : a.D % 2 == 0 ? f<bf16, float, false, 2, 4>(a, s)                 \
+                            : f<bf16, float, false, 1, 2>(a, s);                \
+    if (a.sigmoid)                                                              \
+      return a.D % 4 == 0 ? f<float, float, true, 1, 16>(a, s)                  \
+                          : f<float, float, true, 1, 4>(a, s);                  \
+    return a.D % 4 == 0 ? f<float, float, false, 1, 16>(a, s)                   \
+                        : f<float, float, false, 1, 4>(a, s);                   \
+  } while (0)
+
+cudaError_t recur_fwd(const RecurArgs& a, cudaStream_t s) { RECUR_DISPATCH(fwd); }
+cudaError_t recur_bwd(const RecurArgs& a, cudaStream_t s) { RECUR_DISPATCH(bwd); }
 cudaError_t recur_step(const RecurArgs& a, cudaStream_t s) {
   const int vc = a.D % 2 == 0 ? 2 : 1;
   const int cols = kStepThreads * vc;

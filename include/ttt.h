@@ -418,7 +418,8 @@ ttt_status ttt_recur_step(const ttt_recur_config* cfg, const void* X, const void
  *  comes from the unrounded float32 P and is rounded once. residual may be Y (the residual
  *  stream updated in place), and so may mul.
  *  With act = SiLU and mul = H W_up^T this is the gated-MLP activation Z of inplace_ttt_fwd.
- *  Requirements: N % 8 == 0, K % 8 == 0 (else TTT_ERR_UNSUPPORTED); any M >= 1. */
+ *  Requirements: N % 8 == 0, K % 8 == 0 (else TTT_ERR_UNSUPPORTED); M, N, K <= 2^31 - 513 and the
+ *  matrices' elements <= 2^40 each. */
 ttt_status ttt_linear_fwd(int M, int N, int K, int act, const void* X, const void* W,
                           const float* bias, const void* mul, const void* residual, void* Y,
                           void* P, void* workspace, size_t workspace_bytes, void* stream);

@@ -54,6 +54,9 @@ ttt_status check_recur(const ttt_recur_config* c, RecurArgs* a) {
 ttt_status check_linear(int M, int N, int K, int act) {
   if (M < 1 || N < 1 || K < 1) return TTT_ERR_INVALID_ARG;
   if (act != TTT_ACT_ID && act != TTT_ACT_SILU) return TTT_ERR_INVALID_ARG;
+  // tiles reach past the last row: their indices stay below 2^31
+  constexpr int kMax = 2147483647 - 512;
+  if (M > kMax || N > kMax || K > kMax) return TTT_ERR_INVALID_ARG;
   const long long lim = 1ll << 40;
   if ((long long)M * N > lim || (long long)M * K > lim || (long long)N * K > lim)
     return TTT_ERR_INVALID_ARG;

@@ -1,124 +1,679 @@
 // Linear layer with bias, activation, multiplier and residual in its epilogue, forward and
-// backward (include/ttt.h): 64 x 64 tiles on CUDA cores, bf16 operands, float32 sums.
+// backward (include/ttt.h), on the tensor cores.
+//
+// Every product is D[i, j] = sum_k A[i, k] B[j, k] with bf16 operands, each stored with k
+// contiguous (K-major) or with its own index contiguous (MN-major):
+//   forward  P  = X W^T   rows tokens,    columns outputs, k inputs:  X, W K-major
+//   dX = dP W             rows tokens,    columns inputs,  k outputs: dP K-major, W MN-major
+//   dW = dP^T X           rows outputs,   columns inputs,  k tokens:  dP, X MN-major
+// TMA fills what lies outside a matrix with zeros, so that every size is a number of full tiles.
+//
+// Two kernels:
+//   pair: 256 x 256 tiles on CTA pairs (cta_group::2), persistent, two accumulators in TMEM so
+//         that the epilogue of one tile runs under the products of the next. Bound by the tensor
+//         cores.
+//   split: 128 x NT tiles with the roles of rows and columns exchanged (the weights' rows are the
+//         MMA's 128 rows, NT = 16..128 tokens its columns), one tile a CTA and several CTAs an
+//         SM; the CTAs of a cluster share the contraction of one tile and add their parts through
+//         distributed shared memory in a fixed order. For few tiles: decode steps, which read the
+//         weights once (bound by HBM), and small matrices.
 #include <cuda_bf16.h>
-#include <cuda_runtime.h>
 
+#include <algorithm>
+
+#include "common.cuh"
 #include "kernels.h"
-#include "simt_util.cuh"
+#include "pair_tc.cuh"
 
 namespace tttk {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int TS = 64, TK = 16;
+constexpr int kSMs = 148;
+constexpr int BK = 64;  // contraction per stage: one 128-byte swizzled row
 
-// acc[i][j] of rows r0 + 4 ty + i, columns c0 + 4 tx + j of A B with A(m, k), B(k, n) given by
-// strides.
-struct View {
-  const bf16* p;
-  size_t s0, s1;  // strides of the (row or column, k) indices
+// sigmoid with the hardware's exponential and reciprocal: 2 steps of float32 each and one for
+// every unit of |z|, below the bf16 result's half step
+__device__ __forceinline__ float sigm(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// The epilogue: P = D + bias, Y = act(P) mul + residual at [row, col] of a row-major matrix.
+struct Epi {
+  const float* bias;          // by column (pair) or by row (split): the output feature
+  const bf16 *mul, *residual;
+  bf16 *Y, *P;
+  size_t ld;
+  int silu;
 };
-__device__ __forceinline__ void tile_product(const View& A, const View& B, int M, int N, int K,
-                                             int r0, int c0, float (&acc)[4][4]) {
-  __shared__ float sa[TK][TS + 1], sb[TK][TS + 1];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    for (int e = threadIdx.x; e < TS * TK; e += 256) {
-      const int k = e % TK, m = e / TK;
-      sa[k][m] = r0 + m < M && k0 + k < K ? ldf(A.p + (r0 + m) * A.s0 + (k0 + k) * A.s1) : 0.f;
-      sb[k][m] = c0 + m < N && k0 + k < K ? ldf(B.p + (c0 + m) * B.s0 + (k0 + k) * B.s1) : 0.f;
+
+// ================================================================================ pair tiles
+constexpr int PT = 256;  // tile rows and columns
+constexpr int kPairThreads = 320, kEpiWarps = 8;
+constexpr int kPairStages = 6;
+constexpr uint32_t kHalf = 128 * BK * 2;      // 16 KB: this CTA's 128 rows of A, or of B
+constexpr uint32_t kPairStage = 2 * kHalf;
+constexpr uint32_t kTurn = 32 * 32 * 4;       // an epilogue warp's block of the accumulator
+struct __align__(8) PairBars {
+  uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kPairSmem = kPairStages * kPairStage + kEpiWarps * kTurn + sizeof(PairBars) + 1024;
+static_assert(kPairSmem <= 232448, "shared memory of one CTA");
+
+struct PairArgs {
+  int rows, cols, nkb;     // of D; 64-wide blocks of k
+  int tm, tn;              // tiles
+  Epi e;
+  unsigned* err;
+};
+// Tile t: groups of kGroup tile rows, column by column, so that the tiles at work at one time
+// share their rows of A and of B in L2.
+constexpr int kGroup = 8;
+__device__ __forceinline__ void pair_tile(const PairArgs& p, int t, int& m0, int& n0) {
+  const int g = t / (kGroup * p.tn), rem = t - g * kGroup * p.tn;
+  const int gm = min(kGroup, p.tm - g * kGroup), n = rem / gm;
+  m0 = (g * kGroup + rem - n * gm) * PT;
+  n0 = n * PT;
+}
+// A tile's half operand (128 rows of A, or 128 of B) for k block kb.
+template <bool MN>
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* m, uint32_t bar, int r0,
+                                          int kb) {
+  if constexpr (MN) {
+    tma_load_2d_pair(dst, m, bar, r0, kb * BK);
+    tma_load_2d_pair(dst + kHalf / 2, m, bar, r0 + 64, kb * BK);
+  } else {
+    tma_load_2d_pair(dst, m, bar, kb * BK, r0);
+  }
+}
+template <bool MN>
+__device__ __forceinline__ uint64_t operand(uint32_t addr, int kk) {
+  return MN ? sdesc_sw128(addr + kk * 2048, kHalf / 2, 1024) : sdesc_sw128(addr + kk * 32, 16, 1024);
+}
+__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[2 * k] = bf16lo(w[k]), v[2 * k + 1] = bf16hi(w[k]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// Warps: 0 TMA loads, 1 MMA (the leader's), 2-9 epilogue (two per TMEM lane quadrant, 128
+// columns each). The leader's barriers count both CTAs' loads and drained accumulators; commits
+// arrive on both CTAs' stage and accumulator barriers.
+template <bool AMN, bool BMN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                       const __grid_constant__ PairArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  PairBars* bars = reinterpret_cast<PairBars*>(smem + kPairStages * kPairStage + kEpiWarps * kTurn);
+  const uint32_t stage0 = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int half = (int)rank * 128;
+  const int tiles = p.tm * p.tn, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const Abort ab{&bars->abort_flag, p.err};
+#define PB(x) smem_u32(&bars->x)
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(PB(full[s]), 1);
+      mbar_init(PB(empty[s]), 1);
     }
-    __syncthreads();
-    for (int k = 0; k < TK; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][4 * ty + i], sb[k][4 * tx + j], acc[i][j]);
-    __syncthreads();
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(PB(acc_full[a]), 1);
+      mbar_init(PB(acc_empty[a]), 2 * kEpiWarps);
+    }
+    bars->abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&ta);
+    tma_prefetch_desc(&tb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(PB(tmem_base), 2 * PT);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        int m0, n0;
+        pair_tile(p, t, m0, n0);
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!(ok = mbar_wait(PB(empty[s]), ph ^ 1, ab))) break;
+          if (leader) mbar_arrive_expect_tx(PB(full[s]), 2 * kPairStage);
+          const uint32_t bar = peer_addr(PB(full[s]), 0), sa = stage0 + s * kPairStage;
+          pair_load<AMN>(sa, &ta, bar, m0 + half, kb);
+          pair_load<BMN>(sa + kHalf, &tb, bar, n0 + half, kb);
+          if (++s == kPairStages) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      constexpr uint32_t id = idesc_bf16(PT, PT, AMN, BMN);
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        if (!(ok = mbar_wait_cluster(PB(acc_empty[acc]), aph ^ 1, ab))) break;
+        tc_fence_after();
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!(ok = mbar_wait(PB(full[s]), ph, ab))) break;
+          tc_fence_after();
+          const uint32_t sa = stage0 + s * kPairStage;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16_pair(tmem + acc * PT, operand<AMN>(sa, kk), operand<BMN>(sa + kHalf, kk), id,
+                          (kb | kk) != 0);
+          mma_commit_pair(PB(empty[s]));
+          if (++s == kPairStages) { s = 0; ph ^= 1; }
+        }
+        if (ok) mma_commit_pair(PB(acc_full[acc]));
+        if (++acc == 2) { acc = 0; aph ^= 1; }
+      }
+    }
+  } else {
+    // A thread reads a row of the accumulator, but rows of the outputs are written best by
+    // several threads: each 32 x 32 block goes through shared memory (16-byte chunks swizzled by
+    // the row) and comes back as 8 columns of 4 rows a thread, a row's 4 threads side by side.
+    const int q = warp & 3, h = (warp - 2) / 4;
+    float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage + (warp - 2) * kTurn);
+    const int c8 = 8 * (lane % 4), r8 = lane / 4;
+    const Epi& e = p.e;
+    int acc = 0;
+    uint32_t aph = 0;
+    for (int t = first; t < tiles; t += step) {
+      int m0, n0;
+      pair_tile(p, t, m0, n0);
+      m0 += half + q * 32;
+      if (!mbar_wait(PB(acc_full[acc]), aph, ab)) break;
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll 1
+      for (int cb = 4 * h; cb < 4 * h + 4; ++cb) {
+        const int col = n0 + 32 * cb + c8;
+        const bool cok = col < p.cols;  // columns come in eights
+        uint4 mu[4], re[4];
+        float b[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = m0 + 8 * i + r8;
+          const size_t o = (size_t)row * e.ld + col;
+          if (cok && row < p.rows) {
+            if (e.mul) mu[i] = *reinterpret_cast<const uint4*>(e.mul + o);
+            if (e.residual) re[i] = *reinterpret_cast<const uint4*>(e.residual + o);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[k] = 0.f;
+        if (e.bias && cok) {
+          *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(e.bias + col);
+          *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(e.bias + col + 4);
+        }
+        float v[32];
+        tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + cb * 32), v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<float4*>(turn + lane * 32 + ((c ^ (lane & 7)) << 2)) =
+              make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + r8, row = m0 + r;
+          if (!cok || row >= p.rows) continue;
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(
+                turn + r * 32 + (((c8 / 4 + k) ^ (r & 7)) << 2));
+            y[4 * k] = x.x + b[4 * k]; y[4 * k + 1] = x.y + b[4 * k + 1];
+            y[4 * k + 2] = x.z + b[4 * k + 2]; y[4 * k + 3] = x.w + b[4 * k + 3];
+          }
+          const size_t o = (size_t)row * e.ld + col;
+          if (e.P) *reinterpret_cast<uint4*>(e.P + o) = pack8(y);
+          if (e.silu)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] *= sigm(y[k]);
+          float w[8];
+          if (e.mul) {
+            unpack8(mu[i], w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] *= w[k];
+          }
+          if (e.residual) {
+            unpack8(re[i], w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] += w[k];
+          }
+          *reinterpret_cast<uint4*>(e.Y + o) = pack8(y);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(PB(acc_empty[acc]));
+        else mbar_arrive_cluster(peer_addr(PB(acc_empty[acc]), 0));
+      }
+      if (++acc == 2) { acc = 0; aph ^= 1; }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();  // no MMA of the leader still writes the peer's TMEM
+  if (bars->abort_flag) __nanosleep(100000);  // let any load issued before the abort land
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * PT);
+  }
+#undef PB
+}
+
+// =============================================================================== split tiles
+// D^T tiles: 128 rows are "features" f (rows of operand A), NT columns "tokens" t (of B); the
+// output at [t, f] is row-major with f contiguous, so that a warp's 32 rows are one 64-byte piece
+// of a token's row. Warps: 0 TMA, 1 MMA, 2-5 epilogue.
+constexpr int kSplitThreads = 192;
+constexpr int kMaxSplit = 8;
+struct SplitArgs {
+  int feats, toks, nkb;
+  int tf, tt, split;  // tiles of features and of tokens, CTAs of a cluster
+  Epi e;
+  unsigned* err;
+};
+template <int NT>
+struct SplitLayout {
+  static constexpr uint32_t kA = 128 * BK * 2, kB = NT * BK * 2, kStage = kA + kB;
+  static constexpr int kStages = NT <= 32 ? 4 : NT == 64 ? 4 : 3;
+  // the parts of a tile that come from the cluster's CTAs take the stages' place
+  static_assert(kStages * kStage >= NT * 128 * 4, "room for the parts");
+};
+struct __align__(8) SplitBars {
+  uint64_t full[4], empty[4], acc;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+template <int NT>
+constexpr size_t split_smem() { return SplitLayout<NT>::kStages * SplitLayout<NT>::kStage + sizeof(SplitBars) + 1024; }
+
+__device__ __forceinline__ void split_out(const Epi& e, float d, float bias, size_t o) {
+  const float p = d + bias;
+  if (e.P) e.P[o] = __float2bfloat16_rn(p);
+  float y = e.silu ? p * sigm(p) : p;
+  if (e.mul) y *= __bfloat162float(e.mul[o]);
+  if (e.residual) y += __bfloat162float(e.residual[o]);
+  e.Y[o] = __float2bfloat16_rn(y);
+}
+
+template <int NT, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kSplitThreads)
+    linear_split_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                        const __grid_constant__ SplitArgs p) {
+  static_assert(!BMN || NT >= 64, "an MN-major operand comes in panels of 64");
+  using L = SplitLayout<NT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  SplitBars* bars = reinterpret_cast<SplitBars*>(smem + L::kStages * L::kStage);
+  const uint32_t stage0 = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int S = p.split, rank = S > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / S, f0 = (tile % p.tf) * 128, t0 = (tile / p.tf) * NT;
+  const int k_lo = (int)((long long)p.nkb * rank / S), k_hi = (int)((long long)p.nkb * (rank + 1) / S);
+  const Abort ab{&bars->abort_flag, p.err};
+  constexpr uint32_t kCols = NT < 32 ? 32 : NT;
+#define SB(x) smem_u32(&bars->x)
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(SB(full[s]), 1);
+      mbar_init(SB(empty[s]), 1);
+    }
+    mbar_init(SB(acc), 1);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(SB(tmem_base), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  if (warp == 0) {
+    if (lane == 0)
+      for (int kb = k_lo; kb < k_hi; ++kb) {
+        const int i = kb - k_lo, s = i % L::kStages;
+        if (i >= L::kStages && !mbar_wait(SB(empty[s]), (i / L::kStages - 1) & 1, ab)) break;
+        const uint32_t bar = SB(full[s]), sa = stage0 + s * L::kStage, sb = sa + L::kA;
+        mbar_arrive_expect_tx(bar, L::kStage);
+        if constexpr (AMN) {
+          tma_load_2d(sa, &ta, bar, f0, kb * BK);
+          tma_load_2d(sa + 8192, &ta, bar, f0 + 64, kb * BK);
+        } else {
+          tma_load_2d(sa, &ta, bar, kb * BK, f0);
+        }
+        if constexpr (BMN) {
+#pragma unroll
+          for (int j = 0; j < NT / 64; ++j) tma_load_2d(sb + 8192 * j, &tb, bar, t0 + 64 * j, kb * BK);
+        } else {
+          tma_load_2d(sb, &tb, bar, kb * BK, t0);
+        }
+      }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_bf16(128, NT, AMN, BMN);
+      for (int kb = k_lo; kb < k_hi; ++kb) {
+        const int i = kb - k_lo, s = i % L::kStages;
+        if (!mbar_wait(SB(full[s]), (i / L::kStages) & 1, ab)) break;
+        tc_fence_after();
+        const uint32_t sa = stage0 + s * L::kStage, sb = sa + L::kA;
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          mma_bf16_ss(tmem, AMN ? sdesc_sw128(sa + kk * 2048, 8192, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024),
+                      BMN ? sdesc_sw128(sb + kk * 2048, 8192, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024),
+                      id, i > 0 || kk > 0);
+        mma_commit(SB(empty[s]));
+      }
+      mma_commit(SB(acc));
+    }
+  }
+  __syncwarp();
+  const int q = warp & 3, f = f0 + q * 32 + lane;
+  const Epi& e = p.e;
+  const float bias = warp >= 2 && e.bias && f < p.feats ? e.bias[f] : 0.f;
+  bool ok = true;
+  if (warp >= 2) {
+    ok = mbar_wait(SB(acc), 0, ab);
+    __syncwarp();
+    tc_fence_after();
+  }
+  if (S > 1) {
+    // part of CTA c, token j of this CTA's share, feature i: parts[(c share + j) 128 + i]
+    const int share = NT / S;
+    __syncwarp();
+    cluster_sync_all();  // the MMAs of all CTAs have read their stages
+    if (warp >= 2) {
+#pragma unroll
+      for (int c = 0; c < NT / 16; ++c) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(tmem_addr(tmem, q * 32, c * 16), v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int t = c * 16 + j, to = t / share;
+          const uint32_t local = stage0 + (uint32_t)((rank * share + t - to * share) * 128 + q * 32 + lane) * 4;
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(local, to)), "f"(v[j]) : "memory");
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    if (warp >= 2 && f < p.feats && ok) {
+      const float* parts = reinterpret_cast<const float*>(smem) + q * 32 + lane;
+      for (int j = 0; j < share; ++j) {
+        const int t = t0 + rank * share + j;
+        if (t >= p.toks) break;
+        float d = 0.f;
+        for (int c = 0; c < S; ++c) d += parts[(c * share + j) * 128];
+        split_out(e, d, bias, (size_t)t * e.ld + f);
+      }
+    }
+  } else if (warp >= 2 && ok) {
+#pragma unroll 1
+    for (int c = 0; c < NT / 16; ++c) {
+      float v[16];
+      __syncwarp();
+      tmem_ld16(tmem_addr(tmem, q * 32, c * 16), v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int t = t0 + c * 16 + j;
+        if (t < p.toks && f < p.feats) split_out(e, v[j], bias, (size_t)t * e.ld + f);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (bars->abort_flag) __nanosleep(100000);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+#undef SB
+}
+
+// ============================================================================ dP, dmul, dbias
+// One pass over dY, P and mul: dP (rounded to bf16 for the products), dmul, and the column sums
+// of dP for dbias. A thread takes 8 columns of every kRowsY-th row of its CTA's rows; the CTAs'
+// sums go to `part` [gridDim.y, N] and are added in a fixed order.
+constexpr int kDpX = 32, kDpY = 8;
+struct DpArgs {
+  int M, N, rows;  // rows of a CTA
+  int silu;
+  const bf16 *dY, *P, *mul;
+  bf16 *dP, *dmul;  // nullable
+  float* part;      // nullable
+};
+__global__ void __launch_bounds__(kDpX* kDpY) linear_dp_kernel(const DpArgs a) {
+  __shared__ float join[kDpY][kDpX * 8 + 8];
+  const int tx = threadIdx.x % kDpX, ty = threadIdx.x / kDpX;
+  const int col = (blockIdx.x * kDpX + tx) * 8;
+  const long long lo = (long long)blockIdx.y * a.rows, hi = min((long long)a.M, lo + a.rows);
+  float sum[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+  if (col < a.N) {
+#pragma unroll 2
+    for (long long r = lo + ty; r < hi; r += kDpY) {
+      const size_t o = (size_t)r * a.N + col;
+      float dy[8];
+      unpack8(*reinterpret_cast<const uint4*>(a.dY + o), dy);
+      if (a.P) {
+        float p[8], s[8];
+        unpack8(*reinterpret_cast<const uint4*>(a.P + o), p);
+        if (a.silu)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s[k] = sigm(p[k]);
+        if (a.dmul) {
+          float m[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m[k] = dy[k] * (a.silu ? p[k] * s[k] : p[k]);
+          *reinterpret_cast<uint4*>(a.dmul + o) = pack8(m);
+        }
+        if (a.silu)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dy[k] *= s[k] * (1.f + p[k] * (1.f - s[k]));
+        if (a.mul) {
+          float m[8];
+          unpack8(*reinterpret_cast<const uint4*>(a.mul + o), m);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dy[k] *= m[k];
+        }
+        if (a.dP) *reinterpret_cast<uint4*>(a.dP + o) = pack8(dy);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += dy[k];
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) join[ty][tx * 8 + k] = sum[k];
+  __syncthreads();
+  const int c = threadIdx.x;  // kDpX * 8 columns, kDpX * kDpY threads
+  if (blockIdx.x * kDpX * 8 + c < a.N) {
+    float t = 0.f;
+#pragma unroll
+    for (int y = 0; y < kDpY; ++y) t += join[y][c];
+    a.part[(size_t)blockIdx.y * a.N + blockIdx.x * kDpX * 8 + c] = t;
+  }
+}
+static_assert(kDpX * 8 == kDpX * kDpY, "a thread per column in the join");
+__global__ void __launch_bounds__(256) linear_dbias_kernel(const float* part, int n, int N, float* dbias) {
+  __shared__ float join[8][33];
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+  float t = 0.f;
+  if (c < N)
+    for (int i = w; i < n; i += 8) t += part[(size_t)i * N + c];
+  join[w][lane] = t;
+  __syncthreads();
+  if (w == 0 && c < N) {
+    t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += join[i][lane];
+    dbias[c] = t;
   }
 }
 
-__global__ void __launch_bounds__(256) linear_fwd_kernel(const LinearArgs a) {
-  float acc[4][4];
-  const int r0 = blockIdx.y * TS, c0 = blockIdx.x * TS;
-  tile_product({static_cast<const bf16*>(a.X), (size_t)a.K, 1},
-               {static_cast<const bf16*>(a.W), (size_t)a.K, 1}, a.M, a.N, a.K, r0, c0, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + 4 * (threadIdx.x / 16) + i, c = c0 + 4 * (threadIdx.x % 16) + j;
-      if (r >= a.M || c >= a.N) continue;
-      const size_t o = (size_t)r * a.N + c;
-      const float p = acc[i][j] + (a.bias ? a.bias[c] : 0.f);
-      if (a.P) static_cast<bf16*>(a.P)[o] = __float2bfloat16_rn(p);
-      float y = actf(a.silu, p);
-      if (a.mul) y *= ldf(static_cast<const bf16*>(a.mul) + o);
-      if (a.residual) y += ldf(static_cast<const bf16*>(a.residual) + o);
-      static_cast<bf16*>(a.Y)[o] = __float2bfloat16_rn(y);
-    }
+// ------------------------------------------------------------------------------------ launch
+// A product D [rows, cols] = A B^T with contraction k; A is [rows, k] (or [k, rows] when AMN), B
+// [cols, k] (or [k, cols] when BMN). Row-major output, row length e.ld.
+struct Product {
+  const void *A, *B;
+  int rows, cols, k;
+  Epi e;
+  unsigned* err;
+};
+int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
+
+bool operand_map(CUtensorMap* m, const void* p, bool mn, int rows, int k, int box_rows) {
+  return mn ? make_tmap_bf16(m, p, rows, k, rows, 64, 64) : make_tmap_bf16(m, p, k, rows, k, 64, box_rows);
 }
 
-__global__ void __launch_bounds__(256)
-    product_kernel(View A, View B, int M, int N, int K, bf16* out) {
-  float acc[4][4];
-  const int r0 = blockIdx.y * TS, c0 = blockIdx.x * TS;
-  tile_product(A, B, M, N, K, r0, c0, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + 4 * (threadIdx.x / 16) + i, c = c0 + 4 * (threadIdx.x % 16) + j;
-      if (r < M && c < N) out[(size_t)r * N + c] = __float2bfloat16_rn(acc[i][j]);
-    }
+template <typename K>
+cudaError_t with_smem(K kernel, size_t smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// dP (bf16), dmul and the bias gradient; one thread per column.
-__global__ void __launch_bounds__(64) linear_dp_kernel(const LinearArgs a, bf16* dP) {
-  const int c = blockIdx.x * 64 + threadIdx.x;
-  if (c >= a.N) return;
-  float sum = 0.f;
-  for (int r = 0; r < a.M; ++r) {
-    const size_t o = (size_t)r * a.N + c;
-    const float dy = ldf(static_cast<const bf16*>(a.dY) + o);
-    float dp = dy;
-    if (a.P_in) {
-      const float p = ldf(static_cast<const bf16*>(a.P_in) + o);
-      if (a.dmul) static_cast<bf16*>(a.dmul)[o] = __float2bfloat16_rn(dy * actf(a.silu, p));
-      dp *= act1(a.silu, p);
-      if (a.mul) dp *= ldf(static_cast<const bf16*>(a.mul) + o);
-    }
-    dP[o] = __float2bfloat16_rn(dp);
-    sum += dp;
+template <bool AMN, bool BMN>
+cudaError_t run_pair(const Product& g, cudaStream_t s) {
+  CUtensorMap ta, tb;
+  if (!operand_map(&ta, g.A, AMN, g.rows, g.k, 128) || !operand_map(&tb, g.B, BMN, g.cols, g.k, 128))
+    return cudaErrorInvalidValue;
+  PairArgs p{g.rows, g.cols, ceil_div(g.k, BK), ceil_div(g.rows, PT), ceil_div(g.cols, PT), g.e, g.err};
+  const cudaError_t e = with_smem(linear_pair_kernel<AMN, BMN>, kPairSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = (int)std::min((long long)p.tm * p.tn, (long long)kSMs / 2);
+  linear_pair_kernel<AMN, BMN><<<2 * pairs, kPairThreads, kPairSmem, s>>>(ta, tb, p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+// The split kernel takes the columns' operand as its rows.
+template <int NT, bool AMN, bool BMN>
+cudaError_t run_split_nt(const Product& g, cudaStream_t s) {
+  CUtensorMap ta, tb;
+  if (!operand_map(&ta, g.B, BMN, g.cols, g.k, 128) || !operand_map(&tb, g.A, AMN, g.rows, g.k, NT))
+    return cudaErrorInvalidValue;
+  SplitArgs p{g.cols, g.rows, ceil_div(g.k, BK), ceil_div(g.cols, 128), ceil_div(g.rows, NT), 1, g.e, g.err};
+  // enough CTAs for two per SM, each with four blocks of k at least
+  const long long tiles = (long long)p.tf * p.tt;
+  while (p.split < kMaxSplit && tiles * p.split < 2 * kSMs && p.nkb / (2 * p.split) >= 4) p.split *= 2;
+  if (tiles * p.split >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  constexpr size_t smem = split_smem<NT>();
+  cudaError_t e = with_smem(linear_split_kernel<NT, BMN, AMN>, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * p.split));
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = p.split;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = p.split > 1;
+  count_launches(1);
+  e = cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, BMN, AMN>, ta, tb, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool AMN, bool BMN>
+cudaError_t run(const Product& g, cudaStream_t s) {
+  const long long tiles = (long long)ceil_div(g.rows, PT) * ceil_div(g.cols, PT);
+  if (tiles >= kSMs / 2) return run_pair<AMN, BMN>(g, s);
+  if constexpr (!AMN) {
+    if (g.rows <= 16) return run_split_nt<16, AMN, BMN>(g, s);
+    if (g.rows <= 32) return run_split_nt<32, AMN, BMN>(g, s);
   }
-  if (a.dbias) a.dbias[c] = sum;
+  if (g.rows <= 64) return run_split_nt<64, AMN, BMN>(g, s);
+  return run_split_nt<128, AMN, BMN>(g, s);
+}
+
+struct BwdPlan {
+  int bx, by, rows;
+  size_t dp_bytes, part_bytes;
+};
+// The pass over dY: about eight CTAs per SM, each with 32 rows at least.
+BwdPlan bwd_plan(int M, int N) {
+  BwdPlan b;
+  b.bx = ceil_div(N, kDpX * 8);
+  const long long want = std::max(1, 8 * kSMs / b.bx);
+  b.rows = (int)std::min<long long>(M, std::max<long long>(32, (M + want - 1) / want));
+  b.by = ceil_div(M, b.rows);
+  b.dp_bytes = ((size_t)M * N * sizeof(bf16) + 255) & ~(size_t)255;
+  b.part_bytes = (size_t)b.by * N * sizeof(float);
+  return b;
 }
 
 }  // namespace
 
 size_t linear_fwd_workspace(int, int, int) { return 0; }
-size_t linear_bwd_workspace(int M, int N, int) { return (size_t)M * N * 2; }
+size_t linear_bwd_workspace(int M, int N, int) {
+  const BwdPlan b = bwd_plan(M, N);
+  return b.dp_bytes + b.part_bytes;
+}
 
 cudaError_t linear_fwd(const LinearArgs& a, cudaStream_t s) {
-  linear_fwd_kernel<<<dim3((a.N + TS - 1) / TS, (a.M + TS - 1) / TS), 256, 0, s>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  const Epi e{a.bias, static_cast<const bf16*>(a.mul), static_cast<const bf16*>(a.residual),
+              static_cast<bf16*>(a.Y), static_cast<bf16*>(a.P), (size_t)a.N, a.silu};
+  return run<false, false>({a.X, a.W, a.M, a.N, a.K, e, a.err}, s);
 }
 
 cudaError_t linear_bwd(const LinearArgs& a, cudaStream_t s) {
+  const BwdPlan b = bwd_plan(a.M, a.N);
   bf16* dP = static_cast<bf16*>(a.ws);
-  const size_t M = a.M, N = a.N, K = a.K;
-  linear_dp_kernel<<<(a.N + 63) / 64, 64, 0, s>>>(a, dP);
-  count_launches(1);
-  if (a.dX) {
-    product_kernel<<<dim3((K + TS - 1) / TS, (M + TS - 1) / TS), 256, 0, s>>>(
-        {dP, N, 1}, {static_cast<const bf16*>(a.W), 1, K}, a.M, a.K, a.N,
-        static_cast<bf16*>(a.dX));
+  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + b.dp_bytes);
+  const bool products = a.dX || a.dW;
+  // without an activation and a multiplier dP is dY
+  const void* dp = a.P_in ? dP : a.dY;
+  cudaError_t e = cudaSuccess;
+  if (a.dbias || (a.P_in && (products || a.dmul))) {
+    const DpArgs d{a.M, a.N, b.rows, a.silu, static_cast<const bf16*>(a.dY),
+                   static_cast<const bf16*>(a.P_in), static_cast<const bf16*>(a.mul),
+                   products && a.P_in ? dP : nullptr, static_cast<bf16*>(a.dmul), a.dbias ? part : nullptr};
+    linear_dp_kernel<<<dim3(b.bx, b.by), kDpX * kDpY, 0, s>>>(d);
     count_launches(1);
+    if (a.dbias) {
+      linear_dbias_kernel<<<(a.N + 31) / 32, 256, 0, s>>>(part, b.by, a.N, a.dbias);
+      count_launches(1);
+    }
+    e = cudaGetLastError();
   }
-  if (a.dW) {
-    product_kernel<<<dim3((K + TS - 1) / TS, (N + TS - 1) / TS), 256, 0, s>>>(
-        {dP, 1, N}, {static_cast<const bf16*>(a.X), 1, K}, a.N, a.K, a.M,
-        static_cast<bf16*>(a.dW));
-    count_launches(1);
+  if (e == cudaSuccess && a.dX) {
+    const Epi out{nullptr, nullptr, nullptr, static_cast<bf16*>(a.dX), nullptr, (size_t)a.K, 0};
+    e = run<false, true>({dp, a.W, a.M, a.K, a.N, out, a.err}, s);
   }
-  return cudaGetLastError();
+  if (e == cudaSuccess && a.dW) {
+    const Epi out{nullptr, nullptr, nullptr, static_cast<bf16*>(a.dW), nullptr, (size_t)a.K, 0};
+    e = run<true, true>({dp, a.X, a.N, a.K, a.M, out, a.err}, s);
+  }
+  return e;
 }
 
 }  // namespace tttk

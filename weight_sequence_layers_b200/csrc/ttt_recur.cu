@@ -23,6 +23,7 @@
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "kernels.h"
+#include "pair_tc.cuh"
 #include "simt_util.cuh"
 
 namespace tttk {
@@ -155,16 +156,6 @@ struct Joins {  // two buffers in turn: a buffer is written again two joins late
   uint64_t full[2];  // the cluster's maps of the round have arrived in cta and cta_reset
   int abort_flag;
 };
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t remote(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 // Stores to a CTA of the cluster that count their bytes on its barrier: the receiver waits for
 // the data alone, where a release would make every round wait for the outputs' stores too.
 __device__ __forceinline__ void st_async(uint32_t addr, const Map<1>& m, uint32_t bar) {
@@ -179,24 +170,6 @@ __device__ __forceinline__ void st_async(uint32_t addr, const Map<2>& m, uint32_
 __device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];"
                ::"r"(addr), "r"(v), "r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-// As mbar_wait; a wait that runs out is recorded, and the rounds go on without waiting.
-__device__ __forceinline__ void wait_cluster(uint32_t bar, uint32_t parity, const Abort& ab) {
-  if (try_wait_cluster(bar, parity) || *ab.flag) return;
-  const unsigned long long t0 = globaltimer();
-  for (uint32_t it = 1; !try_wait_cluster(bar, parity); ++it)
-    if ((it & 63u) == 0 && (*ab.flag || globaltimer() - t0 > kWaitLimitNs)) {
-      if (!*ab.flag) atomicOr(ab.err, ERR_WAIT_TIMEOUT);
-      *ab.flag = 1;
-      return;
-    }
 }
 // Before the first join: the barriers, and that all CTAs of the cluster have started.
 template <int VC>
@@ -251,11 +224,12 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
     Map<VC> c{all<VC>(1.f), fold<VC>(js.seg[buf], 0, kWarps, rs, all<VC>(0.f))};
 #pragma unroll 2
     for (int s = 0; s < kWarps; ++s) c.A = mul(c.A, js.seg[buf][s][lane].A);
-    const uint32_t bar = remote(full, w);
-    st_async(remote(smem_u32(&js.cta[buf][rank][lane]), w), c, bar);
-    if (lane == 0) st_async(remote(smem_u32(&js.cta_reset[buf][rank]), w), rs, bar);
+    const uint32_t bar = peer_addr(full, w);
+    st_async(peer_addr(smem_u32(&js.cta[buf][rank][lane]), w), c, bar);
+    if (lane == 0) st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), w), rs, bar);
   }
-  wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
+  // a wait that runs out is recorded, and the rounds go on without waiting
+  mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
   const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][lane & (kMaxCluster - 1)]);
   const Vec<VC> in = fold<VC>(js.cta[buf], 0, rank, crs, carry);
   carry = fold<VC>(js.cta[buf], rank, cl, crs, in);

@@ -38,7 +38,7 @@ __device__ __forceinline__ float sigm(float z) { return __fdividef(1.f, 1.f + __
 
 // The epilogue: P = D + bias, Y = act(P) mul + residual at [row, col] of a row-major matrix.
 struct Epi {
-  const float* bias;          // by column (pair) or by row (split): the output feature
+  const float* bias;  // by column
   const bf16 *mul, *residual;
   bf16 *Y, *P;
   size_t ld;
@@ -98,6 +98,28 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                     pack_bf16x2(v[6], v[7]));
+}
+
+// Eight neighbouring outputs from their sums y (w: scratch).
+__device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)[8], const uint4& mu,
+                                        const uint4& re, float (&y)[8], float (&w)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] += b[k];
+  if (e.P) *reinterpret_cast<uint4*>(e.P + o) = pack8(y);
+  if (e.silu)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] *= sigm(y[k]);
+  if (e.mul) {
+    unpack8(mu, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] *= w[k];
+  }
+  if (e.residual) {
+    unpack8(re, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] += w[k];
+  }
+  *reinterpret_cast<uint4*>(e.Y + o) = pack8(y);
 }
 
 // Warps: 0 TMA loads, 1 MMA (the leader's), 2-9 epilogue (two per TMEM lane quadrant, 128
@@ -234,31 +256,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + r8, row = m0 + r;
           if (!cok || row >= p.rows) continue;
-          float y[8];
+          float y[8], w[8];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float4 x = *reinterpret_cast<const float4*>(
                 turn + r * 32 + (((c8 / 4 + k) ^ (r & 7)) << 2));
-            y[4 * k] = x.x + b[4 * k]; y[4 * k + 1] = x.y + b[4 * k + 1];
-            y[4 * k + 2] = x.z + b[4 * k + 2]; y[4 * k + 3] = x.w + b[4 * k + 3];
+            y[4 * k] = x.x; y[4 * k + 1] = x.y; y[4 * k + 2] = x.z; y[4 * k + 3] = x.w;
           }
-          const size_t o = (size_t)row * e.ld + col;
-          if (e.P) *reinterpret_cast<uint4*>(e.P + o) = pack8(y);
-          if (e.silu)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= sigm(y[k]);
-          float w[8];
-          if (e.mul) {
-            unpack8(mu[i], w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= w[k];
-          }
-          if (e.residual) {
-            unpack8(re[i], w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] += w[k];
-          }
-          *reinterpret_cast<uint4*>(e.Y + o) = pack8(y);
+          finish8(e, (size_t)row * e.ld + col, b, mu[i], re[i], y, w);
         }
         __syncwarp();
       }
@@ -297,9 +302,13 @@ struct SplitArgs {
 template <int NT>
 struct SplitLayout {
   static constexpr uint32_t kA = 128 * BK * 2, kB = NT * BK * 2, kStage = kA + kB;
-  static constexpr int kStages = NT <= 32 ? 4 : NT == 64 ? 4 : 3;
-  // the parts of a tile that come from the cluster's CTAs take the stages' place
-  static_assert(kStages * kStage >= NT * 128 * 4, "room for the parts");
+  static constexpr int kStages = NT == 16 ? 3 : NT <= 64 ? 4 : 3;  // two CTAs an SM, three with NT = 16
+  // The parts of a tile that come from the cluster's CTAs: in their own place where that is
+  // small, else over the stages, once all CTAs have read these.
+  static constexpr bool kOwnParts = NT <= 32;
+  static constexpr uint32_t kParts = NT * 128 * 4, kOffParts = kOwnParts ? kStages * kStage : 0;
+  static constexpr uint32_t kOffBars = kStages * kStage + (kOwnParts ? kParts : 0);
+  static_assert(kOwnParts || kStages * kStage >= kParts, "room for the parts");
 };
 struct __align__(8) SplitBars {
   uint64_t full[4], empty[4], acc;
@@ -307,16 +316,7 @@ struct __align__(8) SplitBars {
   int abort_flag;
 };
 template <int NT>
-constexpr size_t split_smem() { return SplitLayout<NT>::kStages * SplitLayout<NT>::kStage + sizeof(SplitBars) + 1024; }
-
-__device__ __forceinline__ void split_out(const Epi& e, float d, float bias, size_t o) {
-  const float p = d + bias;
-  if (e.P) e.P[o] = __float2bfloat16_rn(p);
-  float y = e.silu ? p * sigm(p) : p;
-  if (e.mul) y *= __bfloat162float(e.mul[o]);
-  if (e.residual) y += __bfloat162float(e.residual[o]);
-  e.Y[o] = __float2bfloat16_rn(y);
-}
+constexpr size_t split_smem() { return SplitLayout<NT>::kOffBars + sizeof(SplitBars) + 1024; }
 
 template <int NT, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kSplitThreads)
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  SplitBars* bars = reinterpret_cast<SplitBars*>(smem + L::kStages * L::kStage);
+  SplitBars* bars = reinterpret_cast<SplitBars*>(smem + L::kOffBars);
   const uint32_t stage0 = smem_u32(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int S = p.split, rank = S > 1 ? (int)cluster_rank() : 0;
@@ -336,6 +336,23 @@ __global__ void __launch_bounds__(kSplitThreads)
   const Abort ab{&bars->abort_flag, p.err};
   constexpr uint32_t kCols = NT < 32 ? 32 : NT;
 #define SB(x) smem_u32(&bars->x)
+  auto load = [&](int kb) {
+    const int st = (kb - k_lo) % L::kStages;
+    const uint32_t bar = SB(full[st]), sa = stage0 + st * L::kStage, sb = sa + L::kA;
+    mbar_arrive_expect_tx(bar, L::kStage);
+    if constexpr (AMN) {
+      tma_load_2d(sa, &ta, bar, f0, kb * BK);
+      tma_load_2d(sa + 8192, &ta, bar, f0 + 64, kb * BK);
+    } else {
+      tma_load_2d(sa, &ta, bar, kb * BK, f0);
+    }
+    if constexpr (BMN) {
+#pragma unroll
+      for (int j = 0; j < NT / 64; ++j) tma_load_2d(sb + 8192 * j, &tb, bar, t0 + 64 * j, kb * BK);
+    } else {
+      tma_load_2d(sb, &tb, bar, kb * BK, t0);
+    }
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(SB(full[s]), 1);
@@ -344,34 +361,26 @@ __global__ void __launch_bounds__(kSplitThreads)
     mbar_init(SB(acc), 1);
     bars->abort_flag = 0;
     fence_barrier_init();
+    // the first loads run while the other warps get ready
+    for (int kb = k_lo; kb < min(k_hi, k_lo + L::kStages); ++kb) load(kb);
   }
   if (warp == 1) {
     tmem_alloc(SB(tmem_base), kCols);
     tmem_relinquish();
   }
+  // (a CTA's shared memory may be written by the others once all have started)
+  __syncwarp();
+  if (S > 1 && L::kOwnParts) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   if (warp == 0) {
     if (lane == 0)
-      for (int kb = k_lo; kb < k_hi; ++kb) {
-        const int i = kb - k_lo, s = i % L::kStages;
-        if (i >= L::kStages && !mbar_wait(SB(empty[s]), (i / L::kStages - 1) & 1, ab)) break;
-        const uint32_t bar = SB(full[s]), sa = stage0 + s * L::kStage, sb = sa + L::kA;
-        mbar_arrive_expect_tx(bar, L::kStage);
-        if constexpr (AMN) {
-          tma_load_2d(sa, &ta, bar, f0, kb * BK);
-          tma_load_2d(sa + 8192, &ta, bar, f0 + 64, kb * BK);
-        } else {
-          tma_load_2d(sa, &ta, bar, kb * BK, f0);
-        }
-        if constexpr (BMN) {
-#pragma unroll
-          for (int j = 0; j < NT / 64; ++j) tma_load_2d(sb + 8192 * j, &tb, bar, t0 + 64 * j, kb * BK);
-        } else {
-          tma_load_2d(sb, &tb, bar, kb * BK, t0);
-        }
+      for (int kb = k_lo + L::kStages; kb < k_hi; ++kb) {
+        const int i = kb - k_lo;
+        if (!mbar_wait(SB(empty[i % L::kStages]), (i / L::kStages - 1) & 1, ab)) break;
+        load(kb);
       }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -392,59 +401,86 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
   }
   __syncwarp();
-  const int q = warp & 3, f = f0 + q * 32 + lane;
+  // The outputs of this CTA: its share of the tile's tokens, 8 features (16 bytes) at a time, a
+  // token's 16 pieces side by side. The first items' operands are loaded before the sums are
+  // there.
   const Epi& e = p.e;
-  const float bias = warp >= 2 && e.bias && f < p.feats ? e.bias[f] : 0.f;
-  bool ok = true;
+  const int share = NT / S, first = t0 + rank * share, items = share * 16;
+  constexpr int kBatch = 4;
+  uint4 mu[kBatch], re[kBatch];
+  const int f = f0 + 8 * (threadIdx.x % 16);  // the same piece for all of a thread's items
+  auto fetch = [&](int it0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int it = it0 + u * kSplitThreads, t = first + it / 16;
+      if (it < items && t < p.toks && f < p.feats) {
+        const size_t o = (size_t)t * e.ld + f;
+        if (e.mul) mu[u] = *reinterpret_cast<const uint4*>(e.mul + o);
+        if (e.residual) re[u] = *reinterpret_cast<const uint4*>(e.residual + o);
+      }
+    }
+  };
+  fetch(threadIdx.x);
+  float b[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) b[k] = 0.f;
+  if (e.bias && f < p.feats) {
+    *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(e.bias + f);
+    *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(e.bias + f + 4);
+  }
   if (warp >= 2) {
-    ok = mbar_wait(SB(acc), 0, ab);
+    mbar_wait(SB(acc), 0, ab);
     __syncwarp();
     tc_fence_after();
   }
-  if (S > 1) {
-    // part of CTA c, token j of this CTA's share, feature i: parts[(c share + j) 128 + i]
-    const int share = NT / S;
-    __syncwarp();
-    cluster_sync_all();  // the MMAs of all CTAs have read their stages
-    if (warp >= 2) {
+  __syncwarp();
+  if (S > 1 && L::kOwnParts) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else if (S > 1) cluster_sync_all();  // the MMAs of all CTAs have read their stages
+  else if (!L::kOwnParts) __syncthreads();
+  // part of CTA c, token j of a CTA's share, feature i: parts[(c share + j) 128 + i]
+  if (warp >= 2) {
+    const int q = warp & 3;
 #pragma unroll
-      for (int c = 0; c < NT / 16; ++c) {
-        float v[16];
-        __syncwarp();
-        tmem_ld16(tmem_addr(tmem, q * 32, c * 16), v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int t = c * 16 + j, to = t / share;
-          const uint32_t local = stage0 + (uint32_t)((rank * share + t - to * share) * 128 + q * 32 + lane) * 4;
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(local, to)), "f"(v[j]) : "memory");
-        }
-      }
-    }
-    __syncwarp();
-    cluster_sync_all();
-    if (warp >= 2 && f < p.feats && ok) {
-      const float* parts = reinterpret_cast<const float*>(smem) + q * 32 + lane;
-      for (int j = 0; j < share; ++j) {
-        const int t = t0 + rank * share + j;
-        if (t >= p.toks) break;
-        float d = 0.f;
-        for (int c = 0; c < S; ++c) d += parts[(c * share + j) * 128];
-        split_out(e, d, bias, (size_t)t * e.ld + f);
-      }
-    }
-  } else if (warp >= 2 && ok) {
-#pragma unroll 1
     for (int c = 0; c < NT / 16; ++c) {
+      if (t0 + c * 16 >= p.toks) break;
       float v[16];
-      __syncwarp();
       tmem_ld16(tmem_addr(tmem, q * 32, c * 16), v);
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int t = t0 + c * 16 + j;
-        if (t < p.toks && f < p.feats) split_out(e, v[j], bias, (size_t)t * e.ld + f);
+        const int t = c * 16 + j, to = t / share;
+        const uint32_t local = stage0 + L::kOffParts + (uint32_t)((rank * share + t - to * share) * 128 + q * 32 + lane) * 4;
+        if (t0 + t < p.toks) {
+          if (S > 1)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(local, to)), "f"(v[j]) : "memory");
+          else
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(local), "f"(v[j]) : "memory");
+        }
       }
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+  if (S > 1) cluster_sync_all();
+  else __syncthreads();
+  const float* parts = reinterpret_cast<const float*>(smem + L::kOffParts) + 8 * (threadIdx.x % 16);
+  for (int it0 = threadIdx.x; it0 < items; it0 += kBatch * kSplitThreads) {
+    if (it0 != threadIdx.x) fetch(it0);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int it = it0 + u * kSplitThreads, j = it / 16, t = first + j;
+      if (it >= items || t >= p.toks || f >= p.feats) continue;
+      float y[8], w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = 0.f;
+      for (int c = 0; c < S; ++c) {
+        const float4* x = reinterpret_cast<const float4*>(parts + (c * share + j) * 128);
+        const float4 lo = x[0], hi = x[1];
+        y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
+        y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
+      }
+      const size_t o = (size_t)t * e.ld + f;
+      finish8(e, o, b, mu[u], re[u], y, w);
     }
   }
   tc_fence_before();
@@ -477,39 +513,53 @@ __global__ void __launch_bounds__(kDpX* kDpY) linear_dp_kernel(const DpArgs a) {
   float sum[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) sum[k] = 0.f;
-  if (col < a.N) {
-#pragma unroll 2
-    for (long long r = lo + ty; r < hi; r += kDpY) {
-      const size_t o = (size_t)r * a.N + col;
-      float dy[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.dY + o), dy);
-      if (a.P) {
-        float p[8], s[8];
-        unpack8(*reinterpret_cast<const uint4*>(a.P + o), p);
-        if (a.silu)
+  constexpr int kBatch = 4;  // rows in flight
+  if (col < a.N)
+    for (long long r0 = lo + ty; r0 < hi; r0 += kBatch * kDpY) {
+      uint4 qy[kBatch], qp[kBatch], qm[kBatch];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s[k] = sigm(p[k]);
-        if (a.dmul) {
-          float m[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m[k] = dy[k] * (a.silu ? p[k] * s[k] : p[k]);
-          *reinterpret_cast<uint4*>(a.dmul + o) = pack8(m);
+      for (int u = 0; u < kBatch; ++u) {
+        const long long r = r0 + u * kDpY;
+        const size_t o = (size_t)r * a.N + col;
+        qy[u] = make_uint4(0, 0, 0, 0);
+        if (r < hi) {
+          qy[u] = *reinterpret_cast<const uint4*>(a.dY + o);
+          if (a.P) qp[u] = *reinterpret_cast<const uint4*>(a.P + o);
+          if (a.mul) qm[u] = *reinterpret_cast<const uint4*>(a.mul + o);
         }
-        if (a.silu)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) dy[k] *= s[k] * (1.f + p[k] * (1.f - s[k]));
-        if (a.mul) {
-          float m[8];
-          unpack8(*reinterpret_cast<const uint4*>(a.mul + o), m);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) dy[k] *= m[k];
-        }
-        if (a.dP) *reinterpret_cast<uint4*>(a.dP + o) = pack8(dy);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += dy[k];
+      for (int u = 0; u < kBatch; ++u) {
+        const long long r = r0 + u * kDpY;
+        if (r >= hi) break;
+        const size_t o = (size_t)r * a.N + col;
+        float dy[8];
+        unpack8(qy[u], dy);
+        if (a.P) {
+          float p[8], m[8];
+          unpack8(qp[u], p);
+          if (a.dmul) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m[k] = dy[k] * (a.silu ? p[k] * sigm(p[k]) : p[k]);
+            *reinterpret_cast<uint4*>(a.dmul + o) = pack8(m);
+          }
+          if (a.silu)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float s = sigm(p[k]);
+              dy[k] *= s * (1.f + p[k] * (1.f - s));
+            }
+          if (a.mul) {
+            unpack8(qm[u], m);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dy[k] *= m[k];
+          }
+          if (a.dP) *reinterpret_cast<uint4*>(a.dP + o) = pack8(dy);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += dy[k];
+      }
     }
-  }
   if (!a.part) return;
 #pragma unroll
   for (int k = 0; k < 8; ++k) join[ty][tx * 8 + k] = sum[k];
@@ -527,8 +577,14 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float* part, in
   __shared__ float join[8][33];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   float t = 0.f;
-  if (c < N)
-    for (int i = w; i < n; i += 8) t += part[(size_t)i * N + c];
+  if (c < N) {
+    float u[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = w; i < n; i += 32)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + 8 * k < n) u[k] += part[(size_t)(i + 8 * k) * N + c];
+    t = (u[0] + u[1]) + (u[2] + u[3]);
+  }
   join[w][lane] = t;
   __syncthreads();
   if (w == 0 && c < N) {
@@ -580,9 +636,11 @@ cudaError_t run_split_nt(const Product& g, cudaStream_t s) {
   if (!operand_map(&ta, g.B, BMN, g.cols, g.k, 128) || !operand_map(&tb, g.A, AMN, g.rows, g.k, NT))
     return cudaErrorInvalidValue;
   SplitArgs p{g.cols, g.rows, ceil_div(g.k, BK), ceil_div(g.cols, 128), ceil_div(g.rows, NT), 1, g.e, g.err};
-  // enough CTAs for two per SM, each with four blocks of k at least
-  const long long tiles = (long long)p.tf * p.tt;
-  while (p.split < kMaxSplit && tiles * p.split < 2 * kSMs && p.nkb / (2 * p.split) >= 4) p.split *= 2;
+  // As many CTAs as are resident at a time, each with four blocks of k at least. Wide tiles stop
+  // at about one CTA per SM: their parts cost more than a second CTA brings (200 x 2560 x 2560:
+  // split 4 ways 22.5 us, 8 ways 30.8).
+  const long long tiles = (long long)p.tf * p.tt, most = NT <= 32 ? 2 * kSMs + 29 : kSMs + 29;
+  while (p.split < kMaxSplit && 2 * tiles * p.split <= most && p.nkb / (2 * p.split) >= 4) p.split *= 2;
   if (tiles * p.split >= (1ll << 31)) return cudaErrorInvalidConfiguration;
   constexpr size_t smem = split_smem<NT>();
   cudaError_t e = with_smem(linear_split_kernel<NT, BMN, AMN>, smem);
@@ -605,8 +663,10 @@ cudaError_t run_split_nt(const Product& g, cudaStream_t s) {
 
 template <bool AMN, bool BMN>
 cudaError_t run(const Product& g, cudaStream_t s) {
+  // Few rows, or few tiles that are deep: the contraction is split (200 x 2560 x 2560: 22.5 us
+  // against 26.7; 1537 x 1000 x 520, a shallow one: 22.5 against the pair kernel's 18.4).
   const long long tiles = (long long)ceil_div(g.rows, PT) * ceil_div(g.cols, PT);
-  if (tiles >= kSMs / 2) return run_pair<AMN, BMN>(g, s);
+  if (g.rows > 64 && (tiles > kSMs / 8 || g.k < 24 * BK)) return run_pair<AMN, BMN>(g, s);
   if constexpr (!AMN) {
     if (g.rows <= 16) return run_split_nt<16, AMN, BMN>(g, s);
     if (g.rows <= 32) return run_split_nt<32, AMN, BMN>(g, s);
@@ -619,11 +679,12 @@ struct BwdPlan {
   int bx, by, rows;
   size_t dp_bytes, part_bytes;
 };
-// The pass over dY: about eight CTAs per SM, each with 32 rows at least.
+// The pass over dY: six CTAs per SM (two rounds of those that are resident), each with 32 rows at
+// least.
 BwdPlan bwd_plan(int M, int N) {
   BwdPlan b;
   b.bx = ceil_div(N, kDpX * 8);
-  const long long want = std::max(1, 8 * kSMs / b.bx);
+  const long long want = std::max(1, 6 * kSMs / b.bx);
   b.rows = (int)std::min<long long>(M, std::max<long long>(32, (M + want - 1) / want));
   b.by = ceil_div(M, b.rows);
   b.dp_bytes = ((size_t)M * N * sizeof(bf16) + 255) & ~(size_t)255;

@@ -101,6 +101,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 }
 
 // Eight neighbouring outputs from their sums y (w: scratch).
+template <bool AUX>
 __device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)[8], const uint4& mu,
                                         const uint4& re, float (&y)[8], float (&w)[8]) {
 #pragma unroll
@@ -109,12 +110,12 @@ __device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)
   if (e.silu)
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] *= sigm(y[k]);
-  if (e.mul) {
+  if (AUX && e.mul) {
     unpack8(mu, w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] *= w[k];
   }
-  if (e.residual) {
+  if (AUX && e.residual) {
     unpack8(re, w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] += w[k];
@@ -125,7 +126,7 @@ __device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)
 // Warps: 0 TMA loads, 1 MMA (the leader's), 2-9 epilogue (two per TMEM lane quadrant, 128
 // columns each). The leader's barriers count both CTAs' loads and drained accumulators; commits
 // arrive on both CTAs' stage and accumulator barriers.
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool AUX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                        const __grid_constant__ PairArgs p) {
@@ -207,9 +208,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    // A thread reads a row of the accumulator, but rows of the outputs are written best by
-    // several threads: each 32 x 32 block goes through shared memory (16-byte chunks swizzled by
-    // the row) and comes back as 8 columns of 4 rows a thread, a row's 4 threads side by side.
+    // A thread reads a row of the accumulator. Alone, an output is written as such, 64 bytes of a
+    // row a thread (16384 x 2048 x 2048: 94 us; 98 by the other way). With a multiplier or a
+    // residual (AUX), rows are read and written best by several threads: each 32 x 32 block goes
+    // through shared memory (16-byte chunks swizzled by the row) and comes back as 8 columns of 4
+    // rows a thread, a row's 4 threads side by side (100 us; 108 row by row).
     const int q = warp & 3, h = (warp - 2) / 4;
     float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage + (warp - 2) * kTurn);
     const int c8 = 8 * (lane % 4), r8 = lane / 4;
@@ -225,6 +228,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
 #pragma unroll 1
       for (int cb = 4 * h; cb < 4 * h + 4; ++cb) {
+        float v[32];
+        if constexpr (!AUX) {
+          tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + cb * 32), v);
+          tmem_wait_ld();
+          const int row = m0 + lane, c0 = n0 + 32 * cb;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int col = c0 + 8 * j;
+            if (row >= p.rows || col >= p.cols) continue;
+            float b[8], y[8], w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = 0.f, y[k] = v[8 * j + k];
+            if (e.bias) {
+              *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(e.bias + col);
+              *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(e.bias + col + 4);
+            }
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            finish8<false>(e, (size_t)row * e.ld + col, b, none, none, y, w);
+          }
+          __syncwarp();
+          continue;
+        }
         const int col = n0 + 32 * cb + c8;
         const bool cok = col < p.cols;  // columns come in eights
         uint4 mu[4], re[4];
@@ -244,7 +269,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(e.bias + col);
           *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(e.bias + col + 4);
         }
-        float v[32];
         tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + cb * 32), v);
         tmem_wait_ld();
 #pragma unroll
@@ -263,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 turn + r * 32 + (((c8 / 4 + k) ^ (r & 7)) << 2));
             y[4 * k] = x.x; y[4 * k + 1] = x.y; y[4 * k + 2] = x.z; y[4 * k + 3] = x.w;
           }
-          finish8(e, (size_t)row * e.ld + col, b, mu[i], re[i], y, w);
+          finish8<true>(e, (size_t)row * e.ld + col, b, mu[i], re[i], y, w);
         }
         __syncwarp();
       }
@@ -480,7 +504,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
       }
       const size_t o = (size_t)t * e.ld + f;
-      finish8(e, o, b, mu[u], re[u], y, w);
+      finish8<true>(e, o, b, mu[u], re[u], y, w);
     }
   }
   tc_fence_before();
@@ -621,10 +645,14 @@ cudaError_t run_pair(const Product& g, cudaStream_t s) {
   if (!operand_map(&ta, g.A, AMN, g.rows, g.k, 128) || !operand_map(&tb, g.B, BMN, g.cols, g.k, 128))
     return cudaErrorInvalidValue;
   PairArgs p{g.rows, g.cols, ceil_div(g.k, BK), ceil_div(g.rows, PT), ceil_div(g.cols, PT), g.e, g.err};
-  const cudaError_t e = with_smem(linear_pair_kernel<AMN, BMN>, kPairSmem);
+  const bool aux = g.e.mul || g.e.residual;
+  if (aux && (AMN || BMN)) return cudaErrorInvalidValue;  // only the forward has them
+  auto kernel = aux && !AMN && !BMN ? linear_pair_kernel<false, false, true>
+                                    : linear_pair_kernel<AMN, BMN, false>;
+  const cudaError_t e = with_smem(kernel, kPairSmem);
   if (e != cudaSuccess) return e;
   const int pairs = (int)std::min((long long)p.tm * p.tn, (long long)kSMs / 2);
-  linear_pair_kernel<AMN, BMN><<<2 * pairs, kPairThreads, kPairSmem, s>>>(ta, tb, p);
+  kernel<<<2 * pairs, kPairThreads, kPairSmem, s>>>(ta, tb, p);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -137,6 +137,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():
+            # current_stream() builds a Stream object: 3.4 us, a quarter of a small call
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -435,8 +438,7 @@ def _tensors(where, *specs):
     Like _ptr, and each tensor must have the dtype and the number of elements that the call's
     sizes give it: the C ABI sees addresses only, and a short buffer would be read or written
     past its end. None and raw integer addresses pass through unchecked."""
-    import torch
-    dev, out = None, []
+    dev, out = -1, []
     for name, t, n, dtype in specs:
         if t is None or isinstance(t, int):
             out.append(t)
@@ -445,20 +447,27 @@ def _tensors(where, *specs):
             raise ValueError(f"{where}: {name} is {t.numel()} x {t.dtype}, expected {n} x {dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous (dense row-major)")
-        if not t.is_cuda:
-            raise ValueError(f"{where}: {name} must be a CUDA tensor")
-        if dev is None:
+        at = t.get_device()
+        if at != dev or at < 0:
+            if not t.is_cuda:
+                raise ValueError(f"{where}: {name} must be a CUDA tensor")
+            import torch
             dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError(f"{where}: {name} is on {t.device}, but the library runs on the "
-                             f"current device cuda:{dev}")
+            if at != dev:
+                raise ValueError(f"{where}: {name} is on {t.device}, but the library runs on the "
+                                 f"current device cuda:{dev}")
         out.append(t.data_ptr())
     return out
 
 
+_TYPES = {}  # filled on first use: torch is imported by the calls that need it
+
+
 def _dtypes(code):
-    import torch
-    return (torch.bfloat16 if code == BF16 else torch.float32), torch.float32
+    if not _TYPES:
+        import torch
+        _TYPES.update({BF16: (torch.bfloat16, torch.float32), F32: (torch.float32, torch.float32)})
+    return _TYPES[BF16 if code == BF16 else F32]
 
 
 def make_norm_config(B, H, T, d, dtype="bf16", token_major=False, eps=1e-5) -> ttt_norm_config:

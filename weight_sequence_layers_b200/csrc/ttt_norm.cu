@@ -27,6 +27,10 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kSMs = 148;
 constexpr int kNarrowThreads = 128;  // CTA of the narrow-row kernels
+constexpr int kNarrowCtas = 4;       // of them on an SM, by registers
+// Threads of the wide-row kernels on an SM, by the floats of a row that a thread holds.
+constexpr int fwd_threads(int floats) { return floats <= 8 ? 1024 : 512; }
+constexpr int bwd_threads(int floats) { return floats <= 8 ? 640 : 512; }
 
 // VEC elements of a row: one 16-byte access, or one element where the width does not keep rows
 // on 16-byte boundaries. Coherent loads, since S may be X or residual and dX may be dS.
@@ -238,7 +242,7 @@ __device__ __forceinline__ void lanes_sum(float (&v)[N]) {
 // loaded ahead while RU are reduced, which keeps enough bytes in flight. RES: with a residual,
 // which doubles a row's bytes.
 template <typename E, int VEC, int NV, int G, int RU, bool RES>
-__global__ void __launch_bounds__(kNarrowThreads)
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
     norm_fwd_narrow(const __grid_constant__ NormArgs a, const Split sp) {
   using F = Frag<E, VEC, NV>;
   constexpr int NG = kNarrowThreads / G, STEP = RU * NG;
@@ -323,7 +327,7 @@ struct Partials {
 };
 
 template <typename E, int VEC, int NV, int G, int RU>
-__global__ void __launch_bounds__(kNarrowThreads)
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
     norm_bwd_narrow(const __grid_constant__ NormArgs a, const Split sp, const Partials pt) {
   using F = Frag<E, VEC, NV>;
   constexpr int NG = kNarrowThreads / G, STEP = RU * NG;
@@ -520,7 +524,7 @@ __device__ __forceinline__ void ring_init(RingBars& bars, const Ring& rg) {
 }
 
 template <typename E, int VEC, int NV>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
     norm_fwd_wide(const __grid_constant__ NormArgs a, const Split sp, const Ring rg) {
   using F = Frag<E, VEC, NV>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -770,7 +774,8 @@ Shape shape_of(const NormArgs& a) {
 
 // CTAs of an SM, from the threads that the kernels' registers leave room for.
 int ctas_per_sm(const Shape& sh, bool bwd) {
-  const int threads = sh.g ? (bwd ? 512 : 640) : sh.nv > 2 ? 512 : bwd ? 640 : 1024;
+  if (sh.g) return kNarrowCtas;
+  const int floats = sh.nv * sh.vec, threads = bwd ? bwd_threads(floats) : fwd_threads(floats);
   return std::max(1, std::min(8, threads / sh.threads));
 }
 // A run of the backward has at least four rows per group, so that the shares of the weight
@@ -855,10 +860,11 @@ struct Bwd {
     const int nsrc = a.dS ? 3 : 2;
     const Ring rg = ring_of(a, sh, nsrc, true);
     const size_t smem = (size_t)rg.stages * nsrc * rg.slot;
-    if constexpr (NV == 1) {
-      if (sh.threads <= 320) return wide_launch(norm_bwd_wide<E, VEC, 1, 2, 320>, a, sh, sp, rg, smem, s);
+    constexpr int RU = NV * VEC <= (VEC == 1 ? 4 : 8) ? 2 : 1;
+    if constexpr (RU == 2) {
+      if (sh.threads <= 320) return wide_launch(norm_bwd_wide<E, VEC, NV, RU, 320>, a, sh, sp, rg, smem, s);
     }
-    return wide_launch(norm_bwd_wide<E, VEC, NV, NV == 1 ? 2 : 1, 512>, a, sh, sp, rg, smem, s);
+    return wide_launch(norm_bwd_wide<E, VEC, NV, RU, 512>, a, sh, sp, rg, smem, s);
   }
   template <typename K>
   static cudaError_t wide_launch(K kernel, const NormArgs& a, const Shape& sh, const Split& sp,

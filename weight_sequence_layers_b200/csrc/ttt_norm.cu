@@ -443,32 +443,31 @@ struct RowView {
   uint32_t off;  // bytes from the slot's start to the row
   int in_slot;   // elements of the row that the slot holds
 };
+// The view of a row that starts at element x of a tensor of `total` elements.
 template <typename E, int VEC>
-__device__ __forceinline__ RowView row_view(size_t row, int d, size_t total_rows) {
+__device__ __forceinline__ RowView row_view(size_t x, int d, size_t total) {
   if (VEC > 1) return {0u, d};
-  const size_t b0 = row * d * sizeof(E), end = total_rows * d * sizeof(E) & ~(size_t)15;
+  const size_t b0 = x * sizeof(E), end = total * sizeof(E) & ~(size_t)15;
   const size_t held = end > b0 ? (end - b0) / sizeof(E) : 0;
   return {(uint32_t)(b0 & 15), held < (size_t)d ? (int)held : d};
 }
-// Bytes that the copy of a row moves.
+// Bytes that its copy moves.
 template <typename E, int VEC>
-__device__ __forceinline__ uint32_t row_bytes(size_t row, int d, size_t total_rows) {
-  const size_t es = sizeof(E), b0 = row * d * es;
+__device__ __forceinline__ uint32_t row_bytes(size_t x, int d, size_t total) {
+  const size_t es = sizeof(E), b0 = x * es;
   if (VEC > 1) return (uint32_t)(d * es);
-  const size_t from = b0 & ~(size_t)15, end = total_rows * d * es & ~(size_t)15;
+  const size_t from = b0 & ~(size_t)15, end = total * es & ~(size_t)15;
   const size_t to = (b0 + d * es + 15) & ~(size_t)15;
   const size_t stop = to < end ? to : end;
   return stop > from ? (uint32_t)(stop - from) : 0u;
 }
 template <typename E>
-__device__ __forceinline__ void row_copy(uint32_t slot, const E* base, size_t row, int d,
-                                         uint32_t bytes, uint32_t bar) {
+__device__ __forceinline__ void row_copy(uint32_t slot, const E* row, uint32_t bytes, uint32_t bar) {
   if (!bytes) return;
-  const char* src =
-      reinterpret_cast<const char*>(base) + (row * d * sizeof(E) & ~(size_t)15);
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(slot), "l"(src), "r"(bytes), "r"(bar) : "memory");
+      ::"r"(slot), "l"(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15), "r"(bytes), "r"(bar)
+      : "memory");
 }
 template <typename E, int VEC, int NV>
 __device__ __forceinline__ void slot_read(const Frag<E, VEC, NV>& f, const uint8_t* slot,
@@ -491,27 +490,42 @@ struct __align__(16) RingBars {
   uint64_t full[kMaxStages];
   int abort_flag;
 };
-// Sums of N values over the CTA (at most 16 warps) through one barrier. Two buffers alternate:
-// nobody writes a buffer before all have passed the barrier of the sum after the one that last
-// read it.
+// Sums of N (1, 2 or 4) values over the CTA (at most 16 warps) through one barrier. Values are
+// halved among the lanes while they are summed (lanes 32/N v .. hold value v), so that N values
+// cost little more than one. Two buffers alternate: nobody writes a buffer before all have passed
+// the barrier of the sum after the one that last read it. Unused warps' entries are zero.
 template <int N>
 __device__ __forceinline__ void cta_sum(float (&v)[N], float (*red)[16]) {
-  lanes_sum<32>(v);
-  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  if (lane == 0)
-#pragma unroll
-    for (int n = 0; n < N; ++n) red[n][wp] = v[n];
-  __syncthreads();
-  const int nw = blockDim.x >> 5;
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    float t = 0.f;
-    for (int k = 0; k < nw; k += 4) {  // the unused warps' entries are zero
-      const float4 q = *reinterpret_cast<const float4*>(&red[n][k]);
-      t += (q.x + q.y) + (q.z + q.w);
-    }
-    v[n] = t;
+  static_assert(N == 1 || N == 2 || N == 4, "N");
+  constexpr int L = 32 / N;  // lanes of a value
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, mine = lane / L;
+  float c;
+  if constexpr (N == 4) {
+    const bool hi = lane & 16, hi2 = lane & 8;
+    const float a0 = (hi ? v[2] : v[0]) + __shfl_xor_sync(~0u, hi ? v[0] : v[2], 16);
+    const float a1 = (hi ? v[3] : v[1]) + __shfl_xor_sync(~0u, hi ? v[1] : v[3], 16);
+    c = (hi2 ? a1 : a0) + __shfl_xor_sync(~0u, hi2 ? a0 : a1, 8);
+  } else if constexpr (N == 2) {
+    const bool hi = lane & 16;
+    c = (hi ? v[1] : v[0]) + __shfl_xor_sync(~0u, hi ? v[0] : v[1], 16);
+  } else {
+    c = v[0];
   }
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
+  if (lane % L == 0) red[mine][wp] = c;
+  __syncthreads();
+  constexpr int P = L < 16 ? L : 16;  // lanes that read a value's 16 entries
+  if constexpr (P == 8) {
+    const float2 q = reinterpret_cast<const float2*>(red[mine])[lane % 8];
+    c = q.x + q.y;
+  } else {
+    c = red[mine][lane % 16];
+  }
+#pragma unroll
+  for (int o = P / 2; o; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = N == 1 ? c : __shfl_sync(~0u, c, n * L);
 }
 __device__ __forceinline__ void ring_init(RingBars& bars, const Ring& rg) {
   for (int k = threadIdx.x; k < 2 * 4 * 16; k += blockDim.x) (&bars.red[0][0][0])[k] = 0.f;
@@ -523,6 +537,61 @@ __device__ __forceinline__ void ring_init(RingBars& bars, const Ring& rg) {
   __syncthreads();
 }
 
+// A walk over a head's rows one by one, in elements: the row's start in the [B, H, T, d] tensors
+// and in Y, and its index for mean and rstd.
+struct RowWalk {
+  int i, t;
+  size_t x, y, row;
+  __device__ __forceinline__ RowWalk(const NormArgs& a, const Rows& R) {
+    Walk w;
+    w.start(R.lo, a.T, a.H, R.h);
+    i = w.i;
+    t = w.t;
+    row = w.row;
+    x = row * a.d;
+    y = y_row(a, R, w) * a.d;
+  }
+  __device__ __forceinline__ void next(const NormArgs& a) {
+    ++i;
+    ++row;
+    x += a.d;
+    y += a.token_major ? (size_t)a.H * a.d : (size_t)a.d;
+    if (a.H > 1 && ++t == a.T) {
+      t = 0;
+      const size_t skip = (size_t)(a.H - 1) * a.T;
+      row += skip;
+      x += skip * a.d;
+      if (!a.token_major) y += skip * a.d;
+    }
+  }
+};
+// Row loads of one thread into the ring, stage after stage.
+template <typename E, int VEC>
+struct Loader {
+  RowWalk at;
+  int st = 0;
+  uint32_t slots, bars;
+  size_t total;  // elements of a tensor
+  __device__ __forceinline__ Loader(const NormArgs& a, const Rows& R, uint32_t slots_, uint32_t bars_)
+      : at(a, R), slots(slots_), bars(bars_), total((size_t)a.B * a.H * a.T * a.d) {}
+  // n rows of the tensors s0, s1 (by x) and sy (by y; each nullable) into the next stages
+  __device__ __forceinline__ void issue(int n, const NormArgs& a, const Rows& R, const Ring& rg,
+                                        const E* s0, const E* sy, const E* s1) {
+    const int nsrc = 1 + (sy != nullptr) + (s1 != nullptr);
+    for (; n > 0 && at.i < R.hi; --n) {
+      const uint32_t nx = row_bytes<E, VEC>(at.x, a.d, total), ny = row_bytes<E, VEC>(at.y, a.d, total);
+      uint32_t slot = slots + st * nsrc * rg.slot;
+      const uint32_t bar = bars + 8 * st;
+      mbar_arrive_expect_tx(bar, nx * (s1 ? 2 : 1) + (sy ? ny : 0));
+      row_copy(slot, s0 + at.x, nx, bar);
+      if (sy) row_copy(slot += rg.slot, sy + at.y, ny, bar);
+      if (s1) row_copy(slot + rg.slot, s1 + at.x, nx, bar);
+      at.next(a);
+      if (++st == rg.stages) st = 0;
+    }
+  }
+};
+
 template <typename E, int VEC, int NV>
 __global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
     norm_fwd_wide(const __grid_constant__ NormArgs a, const Split sp, const Ring rg) {
@@ -533,7 +602,6 @@ __global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
   const int tid = threadIdx.x, d = a.d;
   const F f{tid * VEC, (int)blockDim.x * VEC, d};
   const float inv_d = 1.f / (float)d;
-  const size_t total_rows = (size_t)a.B * a.H * a.T;
   const E* X = static_cast<const E*>(a.X);
   const E* Rs = static_cast<const E*>(a.residual);
   E* Y = static_cast<E*>(a.Y);
@@ -541,57 +609,46 @@ __global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
   const Abort ab{&bars.abort_flag, a.err};
   const int nsrc = Rs ? 2 : 1;
   ring_init(bars, rg);
-  Walk ahead, at;  // the row to load next (one thread) and the row at hand
-  ahead.start(R.lo, a.T, a.H, R.h);
-  at = ahead;
-  auto issue = [&](int st) {
-    const uint32_t n = row_bytes<E, VEC>(ahead.row, d, total_rows);
-    const uint32_t slot = smem_u32(smem) + st * nsrc * rg.slot, bar = smem_u32(&bars.full[st]);
-    mbar_arrive_expect_tx(bar, n * nsrc);
-    row_copy(slot, X, ahead.row, d, n, bar);
-    if (Rs) row_copy(slot + rg.slot, Rs, ahead.row, d, n, bar);
-    ahead.next(1, a.T, a.H);
-  };
-  if (tid == 0)
-    for (int s = 0; s < rg.stages && ahead.i < R.hi; ++s) issue(s);
+  Loader<E, VEC> ld(a, R, smem_u32(smem), smem_u32(bars.full));
+  if (tid == 0) ld.issue(rg.stages, a, R, rg, X, nullptr, Rs);
   float2 w[F::NP], bb[F::NP];
   f.get_f32(a.weight ? a.weight + (size_t)R.h * d : nullptr, 1.f, w);
   f.get_f32(a.bias ? a.bias + (size_t)R.h * d : nullptr, 0.f, bb);
   int st = 0;
   uint32_t ph = 0;
-  for (; at.i < R.hi; at.next(1, a.T, a.H)) {
-    const size_t row = at.row;
-    const RowView rv = row_view<E, VEC>(row, d, total_rows);
+  for (RowWalk at(a, R); at.i < R.hi; at.next(a)) {
+    const RowView rv = row_view<E, VEC>(at.x, d, ld.total);
     const uint8_t* slot = smem + st * nsrc * rg.slot;
     // a wait that runs out is recorded; the loop goes on without waiting, so that all threads
     // keep meeting at the barriers
     mbar_wait(smem_u32(&bars.full[st]), ph, ab);
     float2 v[F::NP];
     float t[1];
-    slot_read(f, slot, rv, X + row * d, v);
+    slot_read(f, slot, rv, X + at.x, v);
     if (Rs) {
       float2 r[F::NP];
-      slot_read(f, slot + rg.slot, rv, Rs + row * d, r);
+      slot_read(f, slot + rg.slot, rv, Rs + at.x, r);
 #pragma unroll
       for (int i = 0; i < F::NP; ++i) v[i] = add2(v[i], r[i]);
     }
     t[0] = total(v);
     cta_sum(t, bars.red[0]);
-    if (tid == 0 && ahead.i < R.hi) issue(st);
+    if (tid == 0) ld.issue(1, a, R, rg, X, nullptr, Rs);
     if (++st == rg.stages) { st = 0; ph ^= 1; }
     const float mean = t[0] * inv_d;
-    if (S) f.store(S + row * d, v);
+    if (S) f.store(S + at.x, v);
     f.centre(mean, v);
     t[0] = total_sq(v);
     cta_sum(t, bars.red[1]);
     const float rstd = rsqrtf(fmaf(t[0], inv_d, a.eps));
     scale_shift(rstd, w, bb, v);
-    f.store(Y + y_row(a, R, at) * d, v);
+    f.store(Y + at.y, v);
     if (tid == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+      if (a.mean) a.mean[at.row] = mean;
+      if (a.rstd) a.rstd[at.row] = rstd;
     }
   }
+  if (bars.abort_flag) __nanosleep(100000);  // let any load issued before the abort land
 }
 
 // RU rows per step share one barrier; a stage is refilled behind the next step's barrier, so that
@@ -608,7 +665,6 @@ __global__ void __launch_bounds__(MAXT, 640 / MAXT)
   const int tid = threadIdx.x, d = a.d;
   const F f{tid * VEC, (int)blockDim.x * VEC, d};
   const float inv_d = 1.f / (float)d;
-  const size_t total_rows = (size_t)a.B * a.H * a.T;
   const E* X = static_cast<const E*>(a.X);
   const E* dY = static_cast<const E*>(a.dY);
   const E* dS = static_cast<const E*>(a.dS);
@@ -616,93 +672,78 @@ __global__ void __launch_bounds__(MAXT, 640 / MAXT)
   const Abort ab{&bars.abort_flag, a.err};
   const int nsrc = dS ? 3 : 2;
   ring_init(bars, rg);
-  Walk ahead, at;
-  ahead.start(R.lo, a.T, a.H, R.h);
-  at = ahead;
-  int ist = 0;  // the stage that the next row loads into
-  auto issue = [&](int n) {
-    for (; n > 0 && ahead.i < R.hi; --n) {
-      const size_t yrow = y_row(a, R, ahead);
-      const uint32_t nx = row_bytes<E, VEC>(ahead.row, d, total_rows);
-      const uint32_t ny = row_bytes<E, VEC>(yrow, d, total_rows);
-      const uint32_t slot = smem_u32(smem) + ist * nsrc * rg.slot;
-      const uint32_t bar = smem_u32(&bars.full[ist]);
-      mbar_arrive_expect_tx(bar, nx * (nsrc - 1) + ny);
-      row_copy(slot, X, ahead.row, d, nx, bar);
-      row_copy(slot + rg.slot, dY, yrow, d, ny, bar);
-      if (dS) row_copy(slot + 2 * rg.slot, dS, ahead.row, d, nx, bar);
-      ahead.next(1, a.T, a.H);
-      if (++ist == rg.stages) ist = 0;
-    }
-  };
-  if (tid == 0) issue(rg.stages);
+  Loader<E, VEC> ld(a, R, smem_u32(smem), smem_u32(bars.full));
+  if (tid == 0) ld.issue(rg.stages, a, R, rg, X, dY, dS);
   float2 w[F::NP], dw[F::NP], db[F::NP];
   f.get_f32(a.weight ? a.weight + (size_t)R.h * d : nullptr, 1.f, w);
 #pragma unroll
   for (int i = 0; i < F::NP; ++i) dw[i] = db[i] = both(0.f);
   int st = 0, buf = 0;
   uint32_t ph = 0;
-  float mean[RU], rstd[RU], nmean[RU], nrstd[RU];
-  Walk stat = at;  // the row whose statistics are read next
+  float nmean[RU], nrstd[RU];
+  RowWalk at(a, R);
+  // the next step's statistics, a step ahead; rows past the run's end read the last row's
+  size_t stat = at.row;
+  int stat_t = at.t, left = R.hi - R.lo;
   auto stats = [&]() {
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
-      nmean[u] = nrstd[u] = 0.f;
-      if (stat.i < R.hi) {
-        nmean[u] = a.mean[stat.row];
-        nrstd[u] = a.rstd[stat.row];
+      nmean[u] = a.mean[stat];
+      nrstd[u] = a.rstd[stat];
+      if (--left > 0) {
+        ++stat;
+        if (a.H > 1 && ++stat_t == a.T) {
+          stat_t = 0;
+          stat += (size_t)(a.H - 1) * a.T;
+        }
       }
-      stat.next(1, a.T, a.H);
     }
   };
-  stats();
+  if (left > 0) stats();
   const bool tight = rg.stages < 2 * RU;
   for (bool first = true; at.i < R.hi; first = false) {  // uniform over the CTA
     float2 xh[RU][F::NP], g[RU][F::NP];
-    float t[2 * RU];
-    size_t row[RU];
+    float t[2 * RU], rstd[RU];
+    size_t x[RU];
     const uint8_t* slot[RU];
     bool live[RU];
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       live[u] = at.i < R.hi;
-      row[u] = at.row;
+      x[u] = at.x;
       slot[u] = smem + st * nsrc * rg.slot;
-      mean[u] = nmean[u];
       rstd[u] = nrstd[u];
       t[2 * u] = t[2 * u + 1] = 0.f;
       if (live[u]) {
-        const size_t yrow = y_row(a, R, at);
         // a wait that runs out is recorded; the loop goes on without waiting, so that all
         // threads keep meeting at the barriers
         mbar_wait(smem_u32(&bars.full[st]), ph, ab);
-        slot_read(f, slot[u], row_view<E, VEC>(row[u], d, total_rows), X + row[u] * d, xh[u]);
-        slot_read(f, slot[u] + rg.slot, row_view<E, VEC>(yrow, d, total_rows), dY + yrow * d, g[u]);
-        bwd_first(mean[u], rstd[u], w, xh[u], g[u], dw, db, t[2 * u], t[2 * u + 1]);
+        slot_read(f, slot[u], row_view<E, VEC>(at.x, d, ld.total), X + at.x, xh[u]);
+        slot_read(f, slot[u] + rg.slot, row_view<E, VEC>(at.y, d, ld.total), dY + at.y, g[u]);
+        bwd_first(nmean[u], rstd[u], w, xh[u], g[u], dw, db, t[2 * u], t[2 * u + 1]);
         if (++st == rg.stages) { st = 0; ph ^= 1; }
+        at.next(a);
       }
-      at.next(1, a.T, a.H);
     }
     stats();
     cta_sum(t, bars.red[buf]);
     buf ^= 1;
-    if (tid == 0 && !first && !tight) issue(RU);  // the last step's rows are all done with
+    if (tid == 0 && !first && !tight) ld.issue(RU, a, R, rg, X, dY, dS);  // the last step's stages
 #pragma unroll
     for (int u = 0; u < RU; ++u)
       if (live[u]) {
         bwd_second(rstd[u], t[2 * u] * inv_d, t[2 * u + 1] * inv_d, xh[u], g[u]);
         if (dS) {
           float2 s[F::NP];
-          slot_read(f, slot[u] + 2 * rg.slot, row_view<E, VEC>(row[u], d, total_rows),
-                    dS + row[u] * d, s);
+          slot_read(f, slot[u] + 2 * rg.slot, row_view<E, VEC>(x[u], d, ld.total), dS + x[u], s);
 #pragma unroll
           for (int i = 0; i < F::NP; ++i) g[u][i] = add2(g[u][i], s[i]);
         }
-        f.store(dX + row[u] * d, g[u]);
+        f.store(dX + x[u], g[u]);
       }
     if (tight) {
       __syncthreads();
-      if (tid == 0) issue(RU);
+      if (tid == 0) ld.issue(RU, a, R, rg, X, dY, dS);
     }
   }
   const size_t base = R.s * pt.ldp + (size_t)R.h * d;
@@ -710,6 +751,7 @@ __global__ void __launch_bounds__(MAXT, 640 / MAXT)
     if (pt.dw0) pt.dw0[base + c] = h ? dw[i].y : dw[i].x;
     if (pt.db0) pt.db0[base + c] = h ? db[i].y : db[i].x;
   });
+  if (bars.abort_flag) __nanosleep(100000);
 }
 
 // dweight[j] = sum over s of part[s][0][j], dbias likewise from part[s][1]: 32 columns per CTA,

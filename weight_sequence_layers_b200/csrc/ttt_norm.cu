@@ -77,30 +77,33 @@ struct Pack<E, 1> {
   __device__ __forceinline__ void load(const E* p) { r = *p; }
 };
 
-// A thread's part of a row: NV accesses of VEC elements, `step` accesses apart, as pairs. VEC = 1
-// has an odd element only with NV = 1 (the pair's second half stays 0). Elements past the
-// row's end read as 0.
+// A thread's part of a row: NV accesses of VEC elements, `step` columns apart, as pairs (VEC = 1
+// has an odd element only with NV = 1: the pair's second half). An access past the row's end
+// reads the row's last elements again (at()): its columns are told apart by mask() only, which
+// costs less than a predicate on every access and value.
 template <typename E, int VEC, int NV>
 struct Frag {
   static constexpr int NP = VEC == 1 ? (NV + 1) / 2 : NV * VEC / 2;  // pairs
   int first, step, d;  // this thread's first column and the columns between its accesses
   __device__ __forceinline__ int col(int n) const { return first + n * step; }
-  __device__ __forceinline__ bool ok(int n) const { return col(n) < d; }
+  __device__ __forceinline__ bool ok(int n) const { return n < NV && col(n) < d; }
+  __device__ __forceinline__ int at(int n) const { return min(col(n), d - VEC); }
+  // 1 for the pair's columns that are the row's, else 0
+  __device__ __forceinline__ void mask(float2 (&m)[NP]) const {
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      m[i] = VEC > 1 ? both(ok(2 * i / VEC) ? 1.f : 0.f)
+                     : make_float2(ok(2 * i) ? 1.f : 0.f, ok(2 * i + 1) ? 1.f : 0.f);
+  }
   // unpacks loaded accesses
   __device__ __forceinline__ void get(const Pack<E, VEC> (&p)[NV], float2 (&v)[NP]) const {
     if constexpr (VEC > 1) {
 #pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        if (ok(n)) p[n].get(v + n * VEC / 2);
-        else
-#pragma unroll
-          for (int k = 0; k < VEC / 2; ++k) v[n * VEC / 2 + k] = both(0.f);
-      }
+      for (int n = 0; n < NV; ++n) p[n].get(v + n * VEC / 2);
     } else {
 #pragma unroll
       for (int n = 0; n < 2 * NP; n += 2)
-        v[n / 2] = make_float2(ok(n) ? ldf(&p[n].r) : 0.f,
-                               n + 1 < NV && ok(n + 1) ? ldf(&p[n + 1 < NV ? n + 1 : 0].r) : 0.f);
+        v[n / 2] = make_float2(ldf(&p[n].r), n + 1 < NV ? ldf(&p[n + 1 < NV ? n + 1 : 0].r) : 0.f);
     }
   }
   template <typename L>
@@ -111,11 +114,11 @@ struct Frag {
 #pragma unroll
         for (int k = 0; k < VEC; ++k) f((n * VEC + k) / 2, (n * VEC + k) & 1, col(n) + k);
   }
+  // float32 parameters of the columns (`none` without an array), 0 past the end
   __device__ __forceinline__ void get_f32(const float* p, float none, float2 (&v)[NP]) const {
 #pragma unroll
-    for (int k = 0; k < NP; ++k) v[k] = both(none);
-    if (!p) return;
-    each_f32([&](int i, int h, int c) { (h ? v[i].y : v[i].x) = p[c]; });
+    for (int k = 0; k < NP; ++k) v[k] = both(0.f);
+    each_f32([&](int i, int h, int c) { (h ? v[i].y : v[i].x) = p ? p[c] : none; });
   }
   __device__ __forceinline__ void store(E* p, const float2 (&v)[NP]) const {
 #pragma unroll
@@ -125,26 +128,20 @@ struct Frag {
         else stf(p + col(n), n & 1 ? v[n / 2].y : v[n / 2].x);
       }
   }
-  // x - mean with elements past the end kept at 0
-  __device__ __forceinline__ void centre(float mean, float2 (&v)[NP]) const {
-    const float2 m = both(-mean);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      if constexpr (VEC > 1) {
-        if (ok(2 * i / VEC)) v[i] = add2(v[i], m);
-      } else {
-        v[i].x = ok(2 * i) ? v[i].x - mean : 0.f;
-        v[i].y = 2 * i + 1 < NV && ok(2 * i + 1) ? v[i].y - mean : 0.f;
-      }
-    }
-  }
 };
+// The masked sum, x - mean (0 past the end), and the sum of squares of that.
 template <int NP>
-__device__ __forceinline__ float total(const float2 (&v)[NP]) {
-  float2 t = v[0];
+__device__ __forceinline__ float total(const float2 (&v)[NP], const float2 (&m)[NP]) {
+  float2 t = mul2(v[0], m[0]);
 #pragma unroll
-  for (int i = 1; i < NP; ++i) t = add2(t, v[i]);
+  for (int i = 1; i < NP; ++i) t = fma2(v[i], m[i], t);
   return t.x + t.y;
+}
+template <int NP>
+__device__ __forceinline__ void centre(float mean, const float2 (&m)[NP], float2 (&v)[NP]) {
+  const float2 c = both(-mean);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) v[i] = fma2(v[i], m[i], mul2(c, m[i]));
 }
 template <int NP>
 __device__ __forceinline__ float total_sq(const float2 (&v)[NP]) {
@@ -161,7 +158,7 @@ __device__ __forceinline__ void scale_shift(float rstd, const float2 (&w)[NP],
   for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(v[i], r), w[i], b[i]);
 }
 // The backward of one row in two halves. first: x -> xh, g (dY) -> g w, the weight gradients'
-// terms, and the sums of g w and g w xh; second: g w -> dX without dS.
+// terms, and the sums of g w and g w xh (w is 0 past the row's end); second: g w -> dX without dS.
 template <int NP>
 __device__ __forceinline__ void bwd_first(float mean, float rstd, const float2 (&w)[NP],
                                           float2 (&x)[NP], float2 (&g)[NP], float2 (&dw)[NP],
@@ -254,7 +251,8 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
   const E* Rs = static_cast<const E*>(a.residual);
   E* Y = static_cast<E*>(a.Y);
   E* S = static_cast<E*>(a.S);
-  float2 w[F::NP], bb[F::NP];
+  float2 w[F::NP], bb[F::NP], mk[F::NP];
+  f.mask(mk);
   Pack<E, VEC> px[RU][NV], pr[RES ? RU : 1][NV];
   Walk at[RU];
   auto fetch = [&]() {
@@ -263,11 +261,10 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
       if (at[u].i < R.hi) {
         const size_t o = at[u].row * d;
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-          if (f.ok(n)) {
-            px[u][n].load(X + o + f.col(n));
-            if constexpr (RES) pr[u][n].load(Rs + o + f.col(n));
-          }
+        for (int n = 0; n < NV; ++n) {
+          px[u][n].load(X + o + f.at(n));
+          if constexpr (RES) pr[u][n].load(Rs + o + f.at(n));
+        }
       }
   };
 #pragma unroll
@@ -293,7 +290,7 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
         for (int i = 0; i < F::NP; ++i) v[u][i] = add2(v[u][i], r[i]);
         if (S && live[u]) f.store(S + row[u] * d, v[u]);
       }
-      t[u] = total(v[u]);
+      t[u] = total(v[u], mk);
       at[u].next(STEP, a.T, a.H);
     }
     fetch();
@@ -301,7 +298,7 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       mean[u] = t[u] * inv_d;
-      f.centre(mean[u], v[u]);
+      centre(mean[u], mk, v[u]);
       t[u] = total_sq(v[u]);
     }
     lanes_sum<G>(t);
@@ -355,12 +352,11 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
         nmean[u] = a.mean[at[u].row];
         nrstd[u] = a.rstd[at[u].row];
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
-          if (f.ok(n)) {
-            px[u][n].load(X + o + f.col(n));
-            py[u][n].load(dY + oy + f.col(n));
-            if (dS) ps[u][n].load(dS + o + f.col(n));
-          }
+        for (int n = 0; n < NV; ++n) {
+          px[u][n].load(X + o + f.at(n));
+          py[u][n].load(dY + oy + f.at(n));
+          if (dS) ps[u][n].load(dS + o + f.at(n));
+        }
       }
     }
   };
@@ -408,7 +404,6 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
       }
   }
   if (!pt.dw0 && !pt.db0) return;
-  // past the row's end the columns hold zeros or, for VEC = 1 pairs, nothing is written
   f.each_f32([&](int i, int h, int c) {
     join[0][grp][c] = h ? dw[i].y : dw[i].x;
     join[1][grp][c] = h ? db[i].y : db[i].x;
@@ -475,12 +470,11 @@ __device__ __forceinline__ void slot_read(const Frag<E, VEC, NV>& f, const uint8
                                           float2 (&v)[Frag<E, VEC, NV>::NP]) {
   Pack<E, VEC> p[NV];
 #pragma unroll
-  for (int n = 0; n < NV; ++n)
-    if (f.ok(n)) {
-      const E* sp = reinterpret_cast<const E*>(slot + rv.off) + f.col(n);
-      if constexpr (VEC == 1) p[n].r = f.col(n) < rv.in_slot ? *sp : row[f.col(n)];
-      else p[n].r = *reinterpret_cast<const decltype(p[n].r)*>(sp);
-    }
+  for (int n = 0; n < NV; ++n) {
+    const E* sp = reinterpret_cast<const E*>(slot + rv.off) + f.at(n);
+    if constexpr (VEC == 1) p[n].r = f.at(n) < rv.in_slot ? *sp : row[f.at(n)];
+    else p[n].r = *reinterpret_cast<const decltype(p[n].r)*>(sp);
+  }
   f.get(p, v);
 }
 
@@ -611,7 +605,8 @@ __global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
   ring_init(bars, rg);
   Loader<E, VEC> ld(a, R, smem_u32(smem), smem_u32(bars.full));
   if (tid == 0) ld.issue(rg.stages, a, R, rg, X, nullptr, Rs);
-  float2 w[F::NP], bb[F::NP];
+  float2 w[F::NP], bb[F::NP], mk[F::NP];
+  f.mask(mk);
   f.get_f32(a.weight ? a.weight + (size_t)R.h * d : nullptr, 1.f, w);
   f.get_f32(a.bias ? a.bias + (size_t)R.h * d : nullptr, 0.f, bb);
   int st = 0;
@@ -631,13 +626,13 @@ __global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
 #pragma unroll
       for (int i = 0; i < F::NP; ++i) v[i] = add2(v[i], r[i]);
     }
-    t[0] = total(v);
+    t[0] = total(v, mk);
     cta_sum(t, bars.red[0]);
     if (tid == 0) ld.issue(1, a, R, rg, X, nullptr, Rs);
     if (++st == rg.stages) { st = 0; ph ^= 1; }
     const float mean = t[0] * inv_d;
     if (S) f.store(S + at.x, v);
-    f.centre(mean, v);
+    centre(mean, mk, v);
     t[0] = total_sq(v);
     cta_sum(t, bars.red[1]);
     const float rstd = rsqrtf(fmaf(t[0], inv_d, a.eps));
@@ -791,7 +786,7 @@ struct Shape {
 };
 // Narrow rows take as few lanes as hold the row in at most two (scalar: eight) accesses each;
 // wide rows one access per thread up to 512 threads, then more accesses.
-Shape shape_of(const NormArgs& a) {
+Shape shape_of(const NormArgs& a, bool bwd) {
   const int v = a.bf16 ? 8 : 4;
   Shape s;
   s.vec = a.d % v == 0 ? v : 1;
@@ -803,11 +798,13 @@ Shape shape_of(const NormArgs& a) {
     if (n <= 32) { s.g = 32; s.nv = 1; return s; }
     if (n <= 64) { s.g = 32; s.nv = 2; return s; }
     s.nv = n <= 512 ? 1 : n <= 1024 ? 2 : n <= 2048 ? 4 : 8;
+    if (bwd && n > 128 && s.nv * s.vec < 16) s.nv = 16 / s.vec;
   } else {
     if (n <= 32) { s.g = 32; s.nv = 1; return s; }
     if (n <= 128) { s.g = 32; s.nv = 4; return s; }
     if (n <= 256) { s.g = 32; s.nv = 8; return s; }
     s.nv = n <= 2048 ? 4 : n <= 4096 ? 8 : 32;
+    if (bwd && s.nv == 4 && n > 512) s.nv = 8;
   }
   s.g = 0;
   s.threads = ((n + s.nv - 1) / s.nv + 31) / 32 * 32;
@@ -866,6 +863,7 @@ Partials partials_of(const NormArgs& a, const Split& sp) {
 }
 
 struct Fwd {
+  static constexpr bool kBwd = false;
   template <typename E, int VEC, int NV, int G, int RU>
   static cudaError_t narrow(const NormArgs& a, const Shape& sh, cudaStream_t s) {
     const Split sp = fwd_split(a, sh);
@@ -889,6 +887,7 @@ struct Fwd {
   }
 };
 struct Bwd {
+  static constexpr bool kBwd = true;
   template <typename E, int VEC, int NV, int G, int RU>
   static cudaError_t narrow(const NormArgs& a, const Shape& sh, cudaStream_t s) {
     const Split sp = bwd_split(a, sh);
@@ -943,7 +942,7 @@ cudaError_t dispatch_scalar(const NormArgs& a, const Shape& sh, cudaStream_t s) 
 }
 template <typename F>
 cudaError_t dispatch(const NormArgs& a, cudaStream_t s) {
-  const Shape sh = shape_of(a);
+  const Shape sh = shape_of(a, F::kBwd);
   count_launches(1);
   if (sh.vec == 8) return dispatch_vec<F, bf16, 8>(a, sh, s);
   if (sh.vec == 4) return dispatch_vec<F, float, 4>(a, sh, s);
@@ -955,7 +954,7 @@ cudaError_t dispatch(const NormArgs& a, cudaStream_t s) {
 bool norm_supported(const NormArgs& a) { return a.d <= 16384; }
 
 size_t norm_bwd_workspace(const NormArgs& a) {
-  const Split sp = bwd_split(a, shape_of(a));
+  const Split sp = bwd_split(a, shape_of(a, true));
   return sp.S == 1 ? 0 : (size_t)sp.S * 2 * a.H * a.d * sizeof(float);
 }
 
@@ -963,7 +962,7 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t s) { return dispatch<Fwd>(a
 
 cudaError_t norm_bwd(const NormArgs& a, cudaStream_t s) {
   cudaError_t e = dispatch<Bwd>(a, s);
-  const Split sp = bwd_split(a, shape_of(a));
+  const Split sp = bwd_split(a, shape_of(a, true));
   if (e != cudaSuccess || sp.S == 1 || !(a.dweight || a.dbias)) return e;
   const size_t cols = (size_t)a.H * a.d;
   cudaLaunchConfig_t cfg{};

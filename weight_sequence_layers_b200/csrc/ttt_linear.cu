@@ -7,6 +7,7 @@
 //   dX = dP W             rows tokens,    columns inputs,  k outputs: dP K-major, W MN-major
 //   dW = dP^T X           rows outputs,   columns inputs,  k tokens:  dP, X MN-major
 // TMA fills what lies outside a matrix with zeros, so that every size is a number of full tiles.
+// A launch takes one product or two (the backward's): both then share the machine.
 //
 // Two kernels:
 //   pair: 256 x 256 tiles on CTA pairs (cta_group::2), persistent, two accumulators in TMEM so
@@ -20,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -48,32 +50,51 @@ struct Epi {
 // ================================================================================ pair tiles
 constexpr int PT = 256;  // tile rows and columns
 constexpr int kPairThreads = 320, kEpiWarps = 8;
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 6, kRing = 4;
+constexpr int kTileReaders = 2 * (1 + kEpiWarps);  // leader: MMA, peer: loads, both: epilogue
 constexpr uint32_t kHalf = 128 * BK * 2;      // 16 KB: this CTA's 128 rows of A, or of B
 constexpr uint32_t kPairStage = 2 * kHalf;
 constexpr uint32_t kTurn = 32 * 32 * 4;       // an epilogue warp's block of the accumulator
 struct __align__(8) PairBars {
-  uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2];
+  uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2], tile_full[kRing],
+      tile_empty[kRing];
+  int ring[kRing];  // tiles handed out, a few ahead
   uint32_t tmem_base;
   int abort_flag;
 };
 constexpr size_t kPairSmem = kPairStages * kPairStage + kEpiWarps * kTurn + sizeof(PairBars) + 1024;
 static_assert(kPairSmem <= 232448, "shared memory of one CTA");
 
-struct PairArgs {
-  int rows, cols, nkb;     // of D; 64-wide blocks of k
-  int tm, tn;              // tiles
+struct PairProb {
+  int rows, cols, nkb;  // of D; 64-wide blocks of k
+  int tm, tn;           // tiles
+  int a_mn, b_mn;
   Epi e;
+};
+// The sums of `part` [n, N] over its rows, which a launch takes along (part: nullable).
+struct Sums {
+  const float* part;
+  int n, N;
+  float* out;
+};
+struct PairArgs {
+  PairProb p[2];
+  int tiles0, tiles;  // of the first product, of both
+  int* counter;       // hands out the tiles; NULL: pair c takes tiles c, c + pairs and so on
+  Sums sums;
   unsigned* err;
 };
 // Tile t: groups of kGroup tile rows, column by column, so that the tiles at work at one time
 // share their rows of A and of B in L2.
 constexpr int kGroup = 8;
-__device__ __forceinline__ void pair_tile(const PairArgs& p, int t, int& m0, int& n0) {
+__device__ __forceinline__ const PairProb& pair_tile(const PairArgs& a, int t, int& m0, int& n0) {
+  const PairProb& p = a.p[t >= a.tiles0];
+  if (t >= a.tiles0) t -= a.tiles0;
   const int g = t / (kGroup * p.tn), rem = t - g * kGroup * p.tn;
   const int gm = min(kGroup, p.tm - g * kGroup), n = rem / gm;
   m0 = (g * kGroup + rem - n * gm) * PT;
   n0 = n * PT;
+  return p;
 }
 // A tile's half operand (128 rows of A, or 128 of B) for k block kb.
 template <bool MN>
@@ -86,9 +107,49 @@ __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* m, ui
     tma_load_2d_pair(dst, m, bar, kb * BK, r0);
   }
 }
+// 128 rows of an operand in a stage, at 16-wide step kk of its block of k.
 template <bool MN>
 __device__ __forceinline__ uint64_t operand(uint32_t addr, int kk) {
   return MN ? sdesc_sw128(addr + kk * 2048, kHalf / 2, 1024) : sdesc_sw128(addr + kk * 32, 16, 1024);
+}
+template <bool MN>
+using Major = std::bool_constant<MN>;
+// f with the operands' layouts as constants: the loops over k that issue loads and products are
+// one thread's, and slow down with descriptors made from run-time layouts (16384 x 2048 x 2048:
+// 96 -> 112 us).
+template <typename F>
+__device__ __forceinline__ bool with_layouts(bool a_mn, bool b_mn, F f) {
+  if (!b_mn) return f(Major<false>{}, Major<false>{});  // the forward
+  if (!a_mn) return f(Major<false>{}, Major<true>{});   // dX
+  return f(Major<true>{}, Major<true>{});               // dW
+}
+// Column sums by W warps (threads 0.. of `tid`), 32 columns at a time. A column's rows fall to
+// eight parts whatever W is, so that the order of the sum is the same in every kernel.
+constexpr int kSumParts = 8;
+template <int W>
+__device__ __forceinline__ void column_sums(const Sums& s, int tid, int block, int blocks, float* join) {
+  const int lane = tid % 32, w = tid / 32;
+  for (int c0 = 32 * block; c0 < s.N; c0 += 32 * blocks) {
+    const int c = c0 + lane;
+#pragma unroll
+    for (int v = w; v < kSumParts; v += W) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      if (c < s.N)
+        for (int i = v; i < s.n; i += 4 * kSumParts)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (i + k * kSumParts < s.n) t[k] += s.part[(size_t)(i + k * kSumParts) * s.N + c];
+      join[v * 32 + lane] = (t[0] + t[1]) + (t[2] + t[3]);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+    if (w == 0 && c < s.N) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSumParts; ++i) sum += join[i * 32 + lane];
+      s.out[c] = sum;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+  }
 }
 __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -99,7 +160,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                     pack_bf16x2(v[6], v[7]));
 }
-
 // Eight neighbouring outputs from their sums y (w: scratch).
 template <bool AUX>
 __device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)[8], const uint4& mu,
@@ -125,10 +185,12 @@ __device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)
 
 // Warps: 0 TMA loads, 1 MMA (the leader's), 2-9 epilogue (two per TMEM lane quadrant, 128
 // columns each). The leader's barriers count both CTAs' loads and drained accumulators; commits
-// arrive on both CTAs' stage and accumulator barriers.
-template <bool AMN, bool BMN, bool AUX>
+// arrive on both CTAs' stage and accumulator barriers. The leader's loading thread takes the
+// tiles and hands each to the roles of both CTAs.
+template <bool AUX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+    linear_pair_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap tb0,
+                       const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap tb1,
                        const __grid_constant__ PairArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -139,7 +201,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int half = (int)rank * 128;
-  const int tiles = p.tm * p.tn, first = blockIdx.x / 2, step = gridDim.x / 2;
   const Abort ab{&bars->abort_flag, p.err};
 #define PB(x) smem_u32(&bars->x)
   if (threadIdx.x == 0) {
@@ -151,10 +212,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(PB(acc_full[a]), 1);
       mbar_init(PB(acc_empty[a]), 2 * kEpiWarps);
     }
+    for (int r = 0; r < kRing; ++r) {
+      mbar_init(PB(tile_full[r]), 1);
+      mbar_init(PB(tile_empty[r]), kTileReaders);
+    }
     bars->abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&ta);
-    tma_prefetch_desc(&tb);
+    tma_prefetch_desc(&ta0);
+    tma_prefetch_desc(&tb0);
+    if (p.tiles > p.tiles0) {
+      tma_prefetch_desc(&ta1);
+      tma_prefetch_desc(&tb1);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(PB(tmem_base), 2 * PT);
@@ -164,45 +233,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what the launch before this one wrote
+  // A reader's next tile; p.tiles or more: none left, or a wait that ran out. Without a counter
+  // all roles know the order, and the ring is not used.
+  int ring = 0, mine = blockIdx.x / 2;
+  uint32_t ring_ph = 0;
+  auto next_tile = [&](bool one_thread) {
+    if (!p.counter) {
+      const int t = mine;
+      mine += gridDim.x / 2;
+      return t;
+    }
+    if (!mbar_wait_cluster(PB(tile_full[ring]), ring_ph, ab)) return 0x7FFFFFFF;
+    const int t = bars->ring[ring];
+    if (!one_thread) __syncwarp();
+    if (one_thread || lane == 0) {
+      if (leader) mbar_arrive(PB(tile_empty[ring]));
+      else mbar_arrive_cluster(peer_addr(PB(tile_empty[ring]), 0));
+    }
+    if (++ring == kRing) { ring = 0; ring_ph ^= 1; }
+    return t;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += step) {
-        int m0, n0;
-        pair_tile(p, t, m0, n0);
-        for (int kb = 0; kb < p.nkb; ++kb) {
-          if (!(ok = mbar_wait(PB(empty[s]), ph ^ 1, ab))) break;
-          if (leader) mbar_arrive_expect_tx(PB(full[s]), 2 * kPairStage);
-          const uint32_t bar = peer_addr(PB(full[s]), 0), sa = stage0 + s * kPairStage;
-          pair_load<AMN>(sa, &ta, bar, m0 + half, kb);
-          pair_load<BMN>(sa + kHalf, &tb, bar, n0 + half, kb);
-          if (++s == kPairStages) { s = 0; ph ^= 1; }
+      while (ok) {
+        int t;
+        if (leader && p.counter) {
+          if (!mbar_wait_cluster(PB(tile_empty[ring]), ring_ph ^ 1, ab)) break;
+          t = atomicAdd(p.counter, 1);
+          bars->ring[ring] = t;
+          st_cluster_u32(peer_addr(PB(ring[ring]), 1), t);
+          mbar_arrive(PB(tile_full[ring]));
+          mbar_arrive_cluster(peer_addr(PB(tile_full[ring]), 1));
+          if (++ring == kRing) { ring = 0; ring_ph ^= 1; }
+        } else {
+          t = next_tile(true);
         }
+        if (t >= p.tiles) break;
+        int m0, n0;
+        const PairProb& g = pair_tile(p, t, m0, n0);
+        const int nkb = g.nkb;
+        const CUtensorMap *ta = t < p.tiles0 ? &ta0 : &ta1, *tb = t < p.tiles0 ? &tb0 : &tb1;
+        ok = with_layouts(g.a_mn, g.b_mn, [&](auto am, auto bm) {
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!mbar_wait(PB(empty[s]), ph ^ 1, ab)) return false;
+            if (leader) mbar_arrive_expect_tx(PB(full[s]), 2 * kPairStage);
+            const uint32_t bar = peer_addr(PB(full[s]), 0), sa = stage0 + s * kPairStage;
+            pair_load<am.value>(sa, ta, bar, m0 + half, kb);
+            pair_load<bm.value>(sa + kHalf, tb, bar, n0 + half, kb);
+            if (++s == kPairStages) { s = 0; ph ^= 1; }
+          }
+          return true;
+        });
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
-      constexpr uint32_t id = idesc_bf16(PT, PT, AMN, BMN);
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += step) {
+      for (int t; ok && (t = next_tile(true)) < p.tiles;) {
+        const PairProb& g = p.p[t >= p.tiles0];
+        const int nkb = g.nkb;
         if (!(ok = mbar_wait_cluster(PB(acc_empty[acc]), aph ^ 1, ab))) break;
         tc_fence_after();
-        for (int kb = 0; kb < p.nkb; ++kb) {
-          if (!(ok = mbar_wait(PB(full[s]), ph, ab))) break;
-          tc_fence_after();
-          const uint32_t sa = stage0 + s * kPairStage;
+        ok = with_layouts(g.a_mn, g.b_mn, [&](auto am, auto bm) {
+          constexpr uint32_t id = idesc_bf16(PT, PT, am.value, bm.value);
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!mbar_wait(PB(full[s]), ph, ab)) return false;
+            tc_fence_after();
+            const uint32_t sa = stage0 + s * kPairStage;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16_pair(tmem + acc * PT, operand<AMN>(sa, kk), operand<BMN>(sa + kHalf, kk), id,
-                          (kb | kk) != 0);
-          mma_commit_pair(PB(empty[s]));
-          if (++s == kPairStages) { s = 0; ph ^= 1; }
-        }
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_bf16_pair(tmem + acc * PT, operand<am.value>(sa, kk), operand<bm.value>(sa + kHalf, kk),
+                            id, (kb | kk) != 0);
+            mma_commit_pair(PB(empty[s]));
+            if (++s == kPairStages) { s = 0; ph ^= 1; }
+          }
+          return true;
+        });
         if (ok) mma_commit_pair(PB(acc_full[acc]));
         if (++acc == 2) { acc = 0; aph ^= 1; }
       }
@@ -216,12 +329,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, h = (warp - 2) / 4;
     float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage + (warp - 2) * kTurn);
     const int c8 = 8 * (lane % 4), r8 = lane / 4;
-    const Epi& e = p.e;
     int acc = 0;
     uint32_t aph = 0;
-    for (int t = first; t < tiles; t += step) {
+    if (p.sums.part) {  // before the first tile's sums are there
+      column_sums<kEpiWarps>(p.sums, threadIdx.x - 64, blockIdx.x, gridDim.x,
+                             reinterpret_cast<float*>(smem + kPairStages * kPairStage));
+    }
+    for (int t; (t = next_tile(false)) < p.tiles;) {
       int m0, n0;
-      pair_tile(p, t, m0, n0);
+      const PairProb& g = pair_tile(p, t, m0, n0);
+      const Epi e = g.e;
+      const int rows = g.rows, cols = g.cols;
       m0 += half + q * 32;
       if (!mbar_wait(PB(acc_full[acc]), aph, ab)) break;
       __syncwarp();
@@ -236,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int col = c0 + 8 * j;
-            if (row >= p.rows || col >= p.cols) continue;
+            if (row >= rows || col >= cols) continue;
             float b[8], y[8], w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) b[k] = 0.f, y[k] = v[8 * j + k];
@@ -251,14 +369,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           continue;
         }
         const int col = n0 + 32 * cb + c8;
-        const bool cok = col < p.cols;  // columns come in eights
+        const bool cok = col < cols;  // columns come in eights
         uint4 mu[4], re[4];
         float b[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = m0 + 8 * i + r8;
           const size_t o = (size_t)row * e.ld + col;
-          if (cok && row < p.rows) {
+          if (cok && row < rows) {
             if (e.mul) mu[i] = *reinterpret_cast<const uint4*>(e.mul + o);
             if (e.residual) re[i] = *reinterpret_cast<const uint4*>(e.residual + o);
           }
@@ -279,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + r8, row = m0 + r;
-          if (!cok || row >= p.rows) continue;
+          if (!cok || row >= rows) continue;
           float y[8], w[8];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -317,10 +435,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // of a token's row. Warps: 0 TMA, 1 MMA, 2-5 epilogue.
 constexpr int kSplitThreads = 192;
 constexpr int kMaxSplit = 8;
-struct SplitArgs {
+struct SplitProb {
   int feats, toks, nkb;
-  int tf, tt, split;  // tiles of features and of tokens, CTAs of a cluster
+  int tf;  // tiles of features
+  int a_mn, b_mn;
   Epi e;
+};
+struct SplitArgs {
+  SplitProb p[2];
+  int tiles0, split;  // tiles of the first product, CTAs of a cluster
+  Sums sums;
   unsigned* err;
 };
 template <int NT>
@@ -338,15 +462,16 @@ struct __align__(8) SplitBars {
   uint64_t full[4], empty[4], acc;
   uint32_t tmem_base;
   int abort_flag;
+  float join[kSumParts * 32];
 };
 template <int NT>
 constexpr size_t split_smem() { return SplitLayout<NT>::kOffBars + sizeof(SplitBars) + 1024; }
 
-template <int NT, bool AMN, bool BMN>
+template <int NT>
 __global__ void __launch_bounds__(kSplitThreads)
-    linear_split_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                        const __grid_constant__ SplitArgs p) {
-  static_assert(!BMN || NT >= 64, "an MN-major operand comes in panels of 64");
+    linear_split_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap tb0,
+                        const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap tb1,
+                        const __grid_constant__ SplitArgs a) {
   using L = SplitLayout<NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -354,27 +479,32 @@ __global__ void __launch_bounds__(kSplitThreads)
   SplitBars* bars = reinterpret_cast<SplitBars*>(smem + L::kOffBars);
   const uint32_t stage0 = smem_u32(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int S = p.split, rank = S > 1 ? (int)cluster_rank() : 0;
-  const int tile = blockIdx.x / S, f0 = (tile % p.tf) * 128, t0 = (tile / p.tf) * NT;
+  const int S = a.split, rank = S > 1 ? (int)cluster_rank() : 0;
+  int tile = blockIdx.x / S;
+  const bool second = tile >= a.tiles0;
+  if (second) tile -= a.tiles0;
+  const SplitProb p = a.p[second];
+  const CUtensorMap *ta = second ? &ta1 : &ta0, *tb = second ? &tb1 : &tb0;
+  const int f0 = (tile % p.tf) * 128, t0 = (tile / p.tf) * NT;
   const int k_lo = (int)((long long)p.nkb * rank / S), k_hi = (int)((long long)p.nkb * (rank + 1) / S);
-  const Abort ab{&bars->abort_flag, p.err};
+  const Abort ab{&bars->abort_flag, a.err};
   constexpr uint32_t kCols = NT < 32 ? 32 : NT;
 #define SB(x) smem_u32(&bars->x)
   auto load = [&](int kb) {
     const int st = (kb - k_lo) % L::kStages;
     const uint32_t bar = SB(full[st]), sa = stage0 + st * L::kStage, sb = sa + L::kA;
     mbar_arrive_expect_tx(bar, L::kStage);
-    if constexpr (AMN) {
-      tma_load_2d(sa, &ta, bar, f0, kb * BK);
-      tma_load_2d(sa + 8192, &ta, bar, f0 + 64, kb * BK);
+    if (p.a_mn) {
+      tma_load_2d(sa, ta, bar, f0, kb * BK);
+      tma_load_2d(sa + 8192, ta, bar, f0 + 64, kb * BK);
     } else {
-      tma_load_2d(sa, &ta, bar, kb * BK, f0);
+      tma_load_2d(sa, ta, bar, kb * BK, f0);
     }
-    if constexpr (BMN) {
+    if (NT >= 64 && p.b_mn) {  // panels of 64
 #pragma unroll
-      for (int j = 0; j < NT / 64; ++j) tma_load_2d(sb + 8192 * j, &tb, bar, t0 + 64 * j, kb * BK);
+      for (int j = 0; j < NT / 64; ++j) tma_load_2d(sb + 8192 * j, tb, bar, t0 + 64 * j, kb * BK);
     } else {
-      tma_load_2d(sb, &tb, bar, kb * BK, t0);
+      tma_load_2d(sb, tb, bar, kb * BK, t0);
     }
   };
   if (threadIdx.x == 0) {
@@ -385,6 +515,9 @@ __global__ void __launch_bounds__(kSplitThreads)
     mbar_init(SB(acc), 1);
     bars->abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(ta);
+    tma_prefetch_desc(tb);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the launch before this one wrote
     // the first loads run while the other warps get ready
     for (int kb = k_lo; kb < min(k_hi, k_lo + L::kStages); ++kb) load(kb);
   }
@@ -408,19 +541,20 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t id = idesc_bf16(128, NT, AMN, BMN);
-      for (int kb = k_lo; kb < k_hi; ++kb) {
-        const int i = kb - k_lo, s = i % L::kStages;
-        if (!mbar_wait(SB(full[s]), (i / L::kStages) & 1, ab)) break;
-        tc_fence_after();
-        const uint32_t sa = stage0 + s * L::kStage, sb = sa + L::kA;
+      with_layouts(p.b_mn, p.a_mn, [&](auto bm, auto am) {  // (its operands are exchanged)
+        constexpr uint32_t id = idesc_bf16(128, NT, am.value, bm.value);
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          const int i = kb - k_lo, s = i % L::kStages;
+          if (!mbar_wait(SB(full[s]), (i / L::kStages) & 1, ab)) return false;
+          tc_fence_after();
+          const uint32_t sa = stage0 + s * L::kStage, sb = sa + L::kA;
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          mma_bf16_ss(tmem, AMN ? sdesc_sw128(sa + kk * 2048, 8192, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024),
-                      BMN ? sdesc_sw128(sb + kk * 2048, 8192, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024),
-                      id, i > 0 || kk > 0);
-        mma_commit(SB(empty[s]));
-      }
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16_ss(tmem, operand<am.value>(sa, kk), operand<bm.value>(sb, kk), id, i > 0 || kk > 0);
+          mma_commit(SB(empty[s]));
+        }
+        return true;
+      });
       mma_commit(SB(acc));
     }
   }
@@ -429,6 +563,10 @@ __global__ void __launch_bounds__(kSplitThreads)
   // token's 16 pieces side by side. The first items' operands are loaded before the sums are
   // there.
   const Epi& e = p.e;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.sums.part && warp >= 2)
+    column_sums<4>(a.sums, threadIdx.x - 64, blockIdx.x, gridDim.x, bars->join);
+  __syncwarp();
   const int share = NT / S, first = t0 + rank * share, items = share * 16;
   constexpr int kBatch = 4;
   uint4 mu[kBatch], re[kBatch];
@@ -463,8 +601,9 @@ __global__ void __launch_bounds__(kSplitThreads)
   else if (!L::kOwnParts) __syncthreads();
   // part of CTA c, token j of a CTA's share, feature i: parts[(c share + j) 128 + i]
   if (warp >= 2) {
-    const int q = warp & 3;
-#pragma unroll
+    const int q = warp & 3, share_log = __ffs(share) - 1;  // the split is a power of two
+    const uint32_t part0 = stage0 + L::kOffParts + (uint32_t)(rank * share * 128 + q * 32 + lane) * 4;
+#pragma unroll 1
     for (int c = 0; c < NT / 16; ++c) {
       if (t0 + c * 16 >= p.toks) break;
       float v[16];
@@ -472,8 +611,8 @@ __global__ void __launch_bounds__(kSplitThreads)
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int t = c * 16 + j, to = t / share;
-        const uint32_t local = stage0 + L::kOffParts + (uint32_t)((rank * share + t - to * share) * 128 + q * 32 + lane) * 4;
+        const int t = c * 16 + j, to = t >> share_log, jj = t & (share - 1);
+        const uint32_t local = part0 + (uint32_t)jj * 512;
         if (t0 + t < p.toks) {
           if (S > 1)
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(local, to)), "f"(v[j]) : "memory");
@@ -528,9 +667,12 @@ struct DpArgs {
   const bf16 *dY, *P, *mul;
   bf16 *dP, *dmul;  // nullable
   float* part;      // nullable
+  int* counter;     // the products' tiles, from 0
 };
 __global__ void __launch_bounds__(kDpX* kDpY) linear_dp_kernel(const DpArgs a) {
   __shared__ float join[kDpY][kDpX * 8 + 8];
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.counter = 0;
   const int tx = threadIdx.x % kDpX, ty = threadIdx.x / kDpX;
   const int col = (blockIdx.x * kDpX + tx) * 8;
   const long long lo = (long long)blockIdx.y * a.rows, hi = min((long long)a.M, lo + a.rows);
@@ -597,36 +739,20 @@ __global__ void __launch_bounds__(kDpX* kDpY) linear_dp_kernel(const DpArgs a) {
   }
 }
 static_assert(kDpX * 8 == kDpX * kDpY, "a thread per column in the join");
-__global__ void __launch_bounds__(256) linear_dbias_kernel(const float* part, int n, int N, float* dbias) {
-  __shared__ float join[8][33];
-  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
-  float t = 0.f;
-  if (c < N) {
-    float u[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = w; i < n; i += 32)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i + 8 * k < n) u[k] += part[(size_t)(i + 8 * k) * N + c];
-    t = (u[0] + u[1]) + (u[2] + u[3]);
-  }
-  join[w][lane] = t;
-  __syncthreads();
-  if (w == 0 && c < N) {
-    t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += join[i][lane];
-    dbias[c] = t;
-  }
+__global__ void __launch_bounds__(256) linear_sums_kernel(const __grid_constant__ Sums s) {
+  __shared__ float join[kSumParts * 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  column_sums<8>(s, threadIdx.x, blockIdx.x, gridDim.x, join);
 }
 
 // ------------------------------------------------------------------------------------ launch
-// A product D [rows, cols] = A B^T with contraction k; A is [rows, k] (or [k, rows] when AMN), B
-// [cols, k] (or [k, cols] when BMN). Row-major output, row length e.ld.
+// A product D [rows, cols] = A B^T with contraction k; A is [rows, k] (or [k, rows] when a_mn), B
+// [cols, k] (or [k, cols] when b_mn). Row-major output, row length e.ld.
 struct Product {
   const void *A, *B;
   int rows, cols, k;
+  bool a_mn, b_mn;
   Epi e;
-  unsigned* err;
 };
 int ceil_div(long long a, int b) { return (int)((a + b - 1) / b); }
 
@@ -634,73 +760,112 @@ bool operand_map(CUtensorMap* m, const void* p, bool mn, int rows, int k, int bo
   return mn ? make_tmap_bf16(m, p, rows, k, rows, 64, 64) : make_tmap_bf16(m, p, k, rows, k, 64, box_rows);
 }
 
-template <typename K>
-cudaError_t with_smem(K kernel, size_t smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
-
-template <bool AMN, bool BMN>
-cudaError_t run_pair(const Product& g, cudaStream_t s) {
-  CUtensorMap ta, tb;
-  if (!operand_map(&ta, g.A, AMN, g.rows, g.k, 128) || !operand_map(&tb, g.B, BMN, g.cols, g.k, 128))
-    return cudaErrorInvalidValue;
-  PairArgs p{g.rows, g.cols, ceil_div(g.k, BK), ceil_div(g.rows, PT), ceil_div(g.cols, PT), g.e, g.err};
-  const bool aux = g.e.mul || g.e.residual;
-  if (aux && (AMN || BMN)) return cudaErrorInvalidValue;  // only the forward has them
-  auto kernel = aux && !AMN && !BMN ? linear_pair_kernel<false, false, true>
-                                    : linear_pair_kernel<AMN, BMN, false>;
-  const cudaError_t e = with_smem(kernel, kPairSmem);
-  if (e != cudaSuccess) return e;
-  const int pairs = (int)std::min((long long)p.tm * p.tn, (long long)kSMs / 2);
-  kernel<<<2 * pairs, kPairThreads, kPairSmem, s>>>(ta, tb, p);
-  count_launches(1);
-  return cudaGetLastError();
-}
-
-// The split kernel takes the columns' operand as its rows.
-template <int NT, bool AMN, bool BMN>
-cudaError_t run_split_nt(const Product& g, cudaStream_t s) {
-  CUtensorMap ta, tb;
-  if (!operand_map(&ta, g.B, BMN, g.cols, g.k, 128) || !operand_map(&tb, g.A, AMN, g.rows, g.k, NT))
-    return cudaErrorInvalidValue;
-  SplitArgs p{g.cols, g.rows, ceil_div(g.k, BK), ceil_div(g.cols, 128), ceil_div(g.rows, NT), 1, g.e, g.err};
-  // As many CTAs as are resident at a time, each with four blocks of k at least. Wide tiles stop
-  // at about one CTA per SM: their parts cost more than a second CTA brings (200 x 2560 x 2560:
-  // split 4 ways 22.5 us, 8 ways 30.8).
-  const long long tiles = (long long)p.tf * p.tt, most = NT <= 32 ? 2 * kSMs + 29 : kSMs + 29;
-  while (p.split < kMaxSplit && 2 * tiles * p.split <= most && p.nkb / (2 * p.split) >= 4) p.split *= 2;
-  if (tiles * p.split >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  constexpr size_t smem = split_smem<NT>();
-  cudaError_t e = with_smem(linear_split_kernel<NT, BMN, AMN>, smem);
+// after: the launch may start before the one in front of it has ended, and waits on the device.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem, int cluster,
+                   bool after, cudaStream_t s, A... args) {
+  cudaError_t e = smem > (48 << 10) ? cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * p.split));
-  cfg.blockDim = dim3(kSplitThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = p.split;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = p.split > 1;
+  cudaLaunchAttribute at[2]{};
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = cluster;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (after) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  cfg.attrs = at;
   count_launches(1);
-  e = cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, BMN, AMN>, ta, tb, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool AMN, bool BMN>
-cudaError_t run(const Product& g, cudaStream_t s) {
-  // Few rows, or few tiles that are deep: the contraction is split (200 x 2560 x 2560: 22.5 us
-  // against 26.7; 1537 x 1000 x 520, a shallow one: 22.5 against the pair kernel's 18.4).
-  const long long tiles = (long long)ceil_div(g.rows, PT) * ceil_div(g.cols, PT);
-  if (g.rows > 64 && (tiles > kSMs / 8 || g.k < 24 * BK)) return run_pair<AMN, BMN>(g, s);
-  if constexpr (!AMN) {
-    if (g.rows <= 16) return run_split_nt<16, AMN, BMN>(g, s);
-    if (g.rows <= 32) return run_split_nt<32, AMN, BMN>(g, s);
+// One or two products (n); the first should be the one with the longer contraction.
+cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bool after,
+                     unsigned* err, cudaStream_t s) {
+  CUtensorMap t[4];
+  PairArgs p{};
+  for (int i = 0; i < 2; ++i) {
+    const Product& q = g[i < n ? i : 0];
+    if (!operand_map(&t[2 * i], q.A, q.a_mn, q.rows, q.k, 128) ||
+        !operand_map(&t[2 * i + 1], q.B, q.b_mn, q.cols, q.k, 128))
+      return cudaErrorInvalidValue;
+    p.p[i] = {q.rows, q.cols, ceil_div(q.k, BK), ceil_div(q.rows, PT), ceil_div(q.cols, PT), q.a_mn, q.b_mn, q.e};
+    if (i < n) p.tiles += p.p[i].tm * p.p[i].tn;
+    if (i == 0) p.tiles0 = p.tiles;
   }
-  if (g.rows <= 64) return run_split_nt<64, AMN, BMN>(g, s);
-  return run_split_nt<128, AMN, BMN>(g, s);
+  p.counter = n > 1 ? counter : nullptr;  // tiles of one product are alike
+  p.sums = sums;
+  p.err = err;
+  const bool aux = g[0].e.mul || g[0].e.residual;
+  return launch(aux ? linear_pair_kernel<true> : linear_pair_kernel<false>,
+                2 * std::min(p.tiles, kSMs / 2), kPairThreads, kPairSmem, 1, after, s, t[0], t[1],
+                t[2], t[3], p);
+}
+
+// The kernel of a product and the CTAs that share a tile's contraction (0: the pair kernel). The
+// choice hangs on the product alone, so that its sums come out the same in any call.
+// Few rows, or few tiles that are deep: the contraction is split (200 x 2560 x 2560: 22.5 us
+// against 26.7; 1537 x 1000 x 520, a shallow one: 22.5 against the pair kernel's 18.4). The
+// backward's shallow products of few rows stay with the pair kernel too: its two then go in one
+// launch.
+int tokens_of(const Product& g) {  // columns of a split tile
+  return !g.a_mn && g.rows <= 16 ? 16 : !g.a_mn && g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128;
+}
+int split_of(const Product& g) {
+  const long long pairs = (long long)ceil_div(g.rows, PT) * ceil_div(g.cols, PT);
+  const int nt = tokens_of(g), nkb = ceil_div(g.k, BK);
+  const long long tiles = (long long)ceil_div(g.rows, nt) * ceil_div(g.cols, 128);
+  if ((g.rows > 64 || g.b_mn) && (pairs > kSMs / 8 || g.k < 24 * BK)) return 0;
+  // As many CTAs as are resident at a time, each with four blocks of k at least. Wide tiles stop
+  // at about one CTA per SM: their parts cost more than a second CTA brings (200 x 2560 x 2560:
+  // split 4 ways 22.5 us, 8 ways 30.8).
+  const long long most = nt <= 32 ? 2 * kSMs + 29 : kSMs + 29;
+  int split = 1;
+  while (split < kMaxSplit && 2 * tiles * split <= most && nkb / (2 * split) >= 4) split *= 2;
+  return split;
+}
+
+// The split kernel takes the columns' operand as its rows.
+template <int NT>
+cudaError_t run_split_nt(const Product* g, int n, int split, const Sums& sums, bool after,
+                         unsigned* err, cudaStream_t s) {
+  CUtensorMap t[4];
+  SplitArgs p{};
+  long long tiles = 0;
+  for (int i = 0; i < 2; ++i) {
+    const Product& q = g[i < n ? i : 0];
+    if (!operand_map(&t[2 * i], q.B, q.b_mn, q.cols, q.k, 128) ||
+        !operand_map(&t[2 * i + 1], q.A, q.a_mn, q.rows, q.k, NT))
+      return cudaErrorInvalidValue;
+    p.p[i] = {q.cols, q.rows, ceil_div(q.k, BK), ceil_div(q.cols, 128), q.b_mn, q.a_mn, q.e};
+    if (i < n) tiles += (long long)p.p[i].tf * ceil_div(q.rows, NT);
+    if (tiles * split >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+    if (i == 0) p.tiles0 = (int)tiles;
+  }
+  p.split = split;
+  p.sums = sums;
+  p.err = err;
+  return launch(linear_split_kernel<NT>, (unsigned)(tiles * split), kSplitThreads, split_smem<NT>(),
+                split, after, s, t[0], t[1], t[2], t[3], p);
+}
+cudaError_t run_split(const Product* g, int n, int split, const Sums& sums, bool after, unsigned* err,
+                      cudaStream_t s) {
+  const int nt = n > 1 ? std::max(tokens_of(g[0]), tokens_of(g[1])) : tokens_of(g[0]);
+  if (nt == 16) return run_split_nt<16>(g, n, split, sums, after, err, s);
+  if (nt == 32) return run_split_nt<32>(g, n, split, sums, after, err, s);
+  if (nt == 64) return run_split_nt<64>(g, n, split, sums, after, err, s);
+  return run_split_nt<128>(g, n, split, sums, after, err, s);
 }
 
 struct BwdPlan {
@@ -716,7 +881,7 @@ BwdPlan bwd_plan(int M, int N) {
   b.rows = (int)std::min<long long>(M, std::max<long long>(32, (M + want - 1) / want));
   b.by = ceil_div(M, b.rows);
   b.dp_bytes = ((size_t)M * N * sizeof(bf16) + 255) & ~(size_t)255;
-  b.part_bytes = (size_t)b.by * N * sizeof(float);
+  b.part_bytes = ((size_t)b.by * N * sizeof(float) + 255) & ~(size_t)255;
   return b;
 }
 
@@ -725,44 +890,61 @@ BwdPlan bwd_plan(int M, int N) {
 size_t linear_fwd_workspace(int, int, int) { return 0; }
 size_t linear_bwd_workspace(int M, int N, int) {
   const BwdPlan b = bwd_plan(M, N);
-  return b.dp_bytes + b.part_bytes;
+  return b.dp_bytes + b.part_bytes + 256;  // and the tile counter
 }
 
 cudaError_t linear_fwd(const LinearArgs& a, cudaStream_t s) {
   const Epi e{a.bias, static_cast<const bf16*>(a.mul), static_cast<const bf16*>(a.residual),
               static_cast<bf16*>(a.Y), static_cast<bf16*>(a.P), (size_t)a.N, a.silu};
-  return run<false, false>({a.X, a.W, a.M, a.N, a.K, e, a.err}, s);
+  const Product g{a.X, a.W, a.M, a.N, a.K, false, false, e};
+  const int split = split_of(g);
+  return split ? run_split(&g, 1, split, {}, false, a.err, s)
+               : run_pair(&g, 1, nullptr, {}, false, a.err, s);
 }
 
 cudaError_t linear_bwd(const LinearArgs& a, cudaStream_t s) {
   const BwdPlan b = bwd_plan(a.M, a.N);
   bf16* dP = static_cast<bf16*>(a.ws);
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + b.dp_bytes);
-  const bool products = a.dX || a.dW;
+  int* counter = reinterpret_cast<int*>(static_cast<char*>(a.ws) + b.dp_bytes + b.part_bytes);
   // without an activation and a multiplier dP is dY
   const void* dp = a.P_in ? dP : a.dY;
-  cudaError_t e = cudaSuccess;
-  if (a.dbias || (a.P_in && (products || a.dmul))) {
+  Product g[2];  // the longer contraction first
+  int n = 0;
+  auto product = [&](void* out, const void* A, const void* B, int rows, int k, bool a_mn) {
+    if (out) g[n++] = {A, B, rows, a.K, k, a_mn, true,
+                       {nullptr, nullptr, nullptr, static_cast<bf16*>(out), nullptr, (size_t)a.K, 0}};
+  };
+  if (a.M < a.N) product(a.dX, dp, a.W, a.M, a.N, false);
+  product(a.dW, dp, a.X, a.N, a.M, true);
+  if (a.M >= a.N) product(a.dX, dp, a.W, a.M, a.N, false);
+  bool after = false;  // a launch of this call is in front of the next one
+  Sums sums{};
+  if (a.dbias || (a.P_in && (n || a.dmul))) {
     const DpArgs d{a.M, a.N, b.rows, a.silu, static_cast<const bf16*>(a.dY),
                    static_cast<const bf16*>(a.P_in), static_cast<const bf16*>(a.mul),
-                   products && a.P_in ? dP : nullptr, static_cast<bf16*>(a.dmul), a.dbias ? part : nullptr};
+                   n && a.P_in ? dP : nullptr, static_cast<bf16*>(a.dmul), a.dbias ? part : nullptr, counter};
     linear_dp_kernel<<<dim3(b.bx, b.by), kDpX * kDpY, 0, s>>>(d);
     count_launches(1);
-    if (a.dbias) {
-      linear_dbias_kernel<<<(a.N + 31) / 32, 256, 0, s>>>(part, b.by, a.N, a.dbias);
-      count_launches(1);
-    }
-    e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.dbias) sums = {part, b.by, a.N, a.dbias};
+    after = true;
   }
-  if (e == cudaSuccess && a.dX) {
-    const Epi out{nullptr, nullptr, nullptr, static_cast<bf16*>(a.dX), nullptr, (size_t)a.K, 0};
-    e = run<false, true>({dp, a.W, a.M, a.K, a.N, out, a.err}, s);
+  int* tiles = after ? counter : nullptr;
+  if (n == 0)
+    return sums.part ? launch(linear_sums_kernel, std::min(ceil_div(a.N, 32), 4 * kSMs), 256, 0, 1, true, s, sums)
+                     : cudaSuccess;
+  const int split[2] = {split_of(g[0]), n > 1 ? split_of(g[1]) : 0};
+  const int together = n > 1 && split[0] == split[1] ? 2 : 1;
+  for (int i = 0; i < n; i += together) {
+    const cudaError_t e = split[i] ? run_split(g + i, together, split[i], sums, after, a.err, s)
+                                   : run_pair(g + i, together, tiles, sums, after, a.err, s);
+    if (e != cudaSuccess) return e;
+    sums = {};
+    after = false;
   }
-  if (e == cudaSuccess && a.dW) {
-    const Epi out{nullptr, nullptr, nullptr, static_cast<bf16*>(a.dW), nullptr, (size_t)a.K, 0};
-    e = run<true, true>({dp, a.X, a.N, a.K, a.M, out, a.err}, s);
-  }
-  return e;
+  return cudaSuccess;
 }
 
 }  // namespace tttk

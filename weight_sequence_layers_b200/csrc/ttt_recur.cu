@@ -240,7 +240,7 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
 template <int VC>
 struct Place {
   int b, c0, c, cl, rank;
-  bool ok;
+  bool ok, two;  // the thread has a feature, has VC of them
   __device__ __forceinline__ Place(const RecurArgs& a, int cluster) {
     cl = cluster;
     rank = cl > 1 ? (int)cluster_rank() : 0;
@@ -249,6 +249,7 @@ struct Place {
     c0 = (i - b * blocks) * 32 * VC;
     c = c0 + (threadIdx.x & 31) * VC;
     ok = c < a.D;
+    two = c + VC <= a.D;
   }
 };
 template <int VC>
@@ -257,13 +258,23 @@ __device__ __forceinline__ Vec<VC> load_state(const float* p, const RecurArgs& a
   if (!p || !at.ok) return all<VC>(0.f);
   p += (size_t)at.b * a.D + at.c;
   if constexpr (VC == 1) return *p;
-  else return make_float2(p[0], p[1]);
+  else return make_float2(p[0], at.two ? p[1] : 0.f);
+}
+// Stores a thread's elements; of an odd row's pairs element by element, `two` of them or one.
+template <typename E, int VC, bool ODD>
+__device__ __forceinline__ void put(E* p, Vec<VC> v, bool two) {
+  if constexpr (ODD && VC == 2) {
+    Raw<E, 1>::store(p, v.x);
+    if (two) Raw<E, 1>::store(p + 1, v.y);
+  } else {
+    Raw<E, VC>::store(p, v);
+  }
 }
 template <int VC>
 __device__ __forceinline__ void store_state(float* p, const RecurArgs& a, const Place<VC>& at,
                                             Vec<VC> v) {
   if (p && at.ok && at.rank == 0 && threadIdx.x < 32)
-    Raw<float, VC>::store(p + (size_t)at.b * a.D + at.c, v);
+    put<float, VC, true>(p + (size_t)at.b * a.D + at.c, v, at.two);
 }
 // The documents' marks of R positions from pos of a walk (position p is token p, or T - 1 - p
 // with REV): lane i loads that of position pos + i.
@@ -276,29 +287,46 @@ __device__ __forceinline__ unsigned load_reset(const RecurArgs& a, int b, unsign
 
 // --------------------------------------------------------------------------------- row loads
 // A warp's R rows of 32 VC elements in shared memory, filled ahead by asynchronous copies of CB
-// bytes (16 where the rows' starts allow it; 2: plain loads, no such copy exists).
-template <typename E, int VC, int R, int CB>
+// bytes: 16 where all rows start on such a boundary, else 4. ODD: rows of an odd number of
+// elements. Of bf16 every second one then starts in the middle of a 4-byte word: the tile holds
+// the words around a row (one more than its own), and `half` (0 or 1) is the element of the first
+// word that the row starts at.
+template <typename E, int VC, int R, int CB, bool ODD>
 struct RowTile {
-  static constexpr int kRow = 32 * VC * (int)sizeof(E), kBytes = R * kRow;
-  // Rows row0, row0 +- D, ...: n of them; `width` elements of each are the tensor's.
+  static constexpr bool kHalves = ODD && sizeof(E) == 2;
+  static constexpr int kRow = 32 * VC * (int)sizeof(E) + (kHalves ? 4 : 0);
+  static constexpr int kBytes = (R * kRow + 15) / 16 * 16;
+  static_assert(!kHalves || VC == 2, "a word per thread");
+  // Rows row0, row0 +- D, ...: n of them; `width` elements of each are the tensor's, which ends at
+  // `end`.
   template <bool REV>
   static __device__ __forceinline__ void fetch(uint32_t dst, const E* row0, unsigned D, int n,
-                                               int width) {
+                                               int width, const E* end) {
     const int lane = threadIdx.x & 31;
-    if constexpr (CB == 2 || (CB == 4 && kRow == 256)) {
-      // one thread, its own VC elements: the pair's two copies, or the plain 2-byte load
+    if constexpr (kHalves) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const E* src = (REV ? rows_back(row0, i, D) : rows(row0, i, D)) + lane * VC;
-        const uint32_t to = dst + i * kRow + lane * VC * (int)sizeof(E);
-        if (i < n && lane * VC < width) {
-          if constexpr (CB == 2) {
-            const unsigned short v = *reinterpret_cast<const unsigned short*>(src);
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
-          } else {
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(src) : "memory");
-          }
-        }
+        const uintptr_t p = reinterpret_cast<uintptr_t>(REV ? rows_back(row0, i, D) : rows(row0, i, D));
+        const int words = ((int)(p & 2) / 2 + min(width, 64) + 1) / 2;
+        const uintptr_t src = (p & ~(uintptr_t)3) + 4 * lane;
+        const uint32_t to = dst + i * kRow + 4 * lane;
+        // the tensor's last word may hold one element only
+        auto copy = [&](uint32_t t, uintptr_t q) {
+          const int bytes = q + 4 <= reinterpret_cast<uintptr_t>(end) ? 4 : 2;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(t), "l"(q), "r"(bytes) : "memory");
+        };
+        if (i < n && lane < words) copy(to, src);
+        if (i < n && lane == 0 && words == 33) copy(to + 128, src + 128);
+      }
+    } else if constexpr (CB == 4 && kRow == 256) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const E* src = (REV ? rows_back(row0, i, D) : rows(row0, i, D)) + lane;
+        const uint32_t to = dst + i * kRow + 4 * lane;
+        if (i < n && lane < width)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(src) : "memory");
+        if (i < n && lane + 32 < width)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 128), "l"(src + 32) : "memory");
       }
     } else {
       constexpr int kLanes = kRow / CB, kStep = 32 / kLanes;
@@ -319,35 +347,45 @@ struct RowTile {
       }
     }
   }
-  static __device__ __forceinline__ Raw<E, VC> get(const uint8_t* tile, int i) {
-    return *reinterpret_cast<const Raw<E, VC>*>(tile + i * kRow + (threadIdx.x & 31) * VC * (int)sizeof(E));
+  static __device__ __forceinline__ Raw<E, VC> get(const uint8_t* tile, int i, int half) {
+    const uint8_t* p = tile + i * kRow + (threadIdx.x & 31) * VC * (int)sizeof(E);
+    if constexpr (kHalves) {
+      const unsigned short* q = reinterpret_cast<const unsigned short*>(p) + half;
+      return {(uint32_t)q[0] | (uint32_t)q[1] << 16};
+    } else {
+      return *reinterpret_cast<const Raw<E, VC>*>(p);
+    }
   }
 };
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-constexpr int kStages = 3;  // rounds in shared memory: the one at hand and two on their way
+// Rounds in shared memory: the one at hand and two on their way; odd rows are a word longer, and two
+// CTAs per SM have room for one round less.
+template <bool ODD>
+constexpr int kStagesOf = ODD ? 2 : 3;
 
 // ----------------------------------------------------------------------------------- forward
-template <typename E, typename GT, int VC, int R, int CB>
+template <typename E, typename GT, int VC, int R, int CB, bool ODD>
 struct FwdTiles {
-  using X = RowTile<E, VC, R, CB>;
-  using G = RowTile<GT, VC, R, sizeof(GT) == 4 && CB < 4 ? 4 : CB>;
+  using X = RowTile<E, VC, R, CB, ODD>;
+  using G = RowTile<GT, VC, R, CB, ODD>;
   static constexpr int kStage = X::kBytes + G::kBytes;  // of one warp
-  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+  static constexpr size_t kSmem = (size_t)kWarps * kStagesOf<ODD> * kStage;
 };
-template <typename E, typename GT, bool SIG, int VC, int R, int CB>
+template <typename E, typename GT, bool SIG, int VC, int R, int CB, bool ODD>
 __global__ void __launch_bounds__(kThreads, 2)
     recur_fwd_kernel(const __grid_constant__ RecurArgs a, const int cluster) {
   using V = Vec<VC>;
-  using Tl = FwdTiles<E, GT, VC, R, CB>;
+  using Tl = FwdTiles<E, GT, VC, R, CB, ODD>;
+  constexpr int kStages = kStagesOf<ODD>;
   extern __shared__ __align__(16) uint8_t tiles[];
   __shared__ Joins<VC> js;
   const Place<VC> at(a, cluster);
   const unsigned T = a.T, D = a.D, stride = (unsigned)at.cl * kWarps * R;
   const int w = threadIdx.x >> 5;
   uint8_t* mine = tiles + w * kStages * Tl::kStage;
-  const size_t base = (size_t)at.b * T * D + at.c0;
+  const size_t base = (size_t)at.b * T * D + at.c0, all_n = (size_t)a.B * T * D;
   const E* X = static_cast<const E*>(a.X) + base;
   const GT* G = static_cast<const GT*>(a.G) + base;
   E* H = static_cast<E*>(a.H) + base + (at.c - at.c0);
@@ -356,8 +394,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (p < T) {
       const int n = min(T - p, (unsigned)R);
       const uint32_t dst = smem_u32(mine) + st * Tl::kStage;
-      Tl::X::template fetch<false>(dst, X + (size_t)p * D, D, n, a.D - at.c0);
-      Tl::G::template fetch<false>(dst + Tl::X::kBytes, G + (size_t)p * D, D, n, a.D - at.c0);
+      Tl::X::template fetch<false>(dst, X + (size_t)p * D, D, n, a.D - at.c0, static_cast<const E*>(a.X) + all_n);
+      Tl::G::template fetch<false>(dst + Tl::X::kBytes, G + (size_t)p * D, D, n, a.D - at.c0,
+                                   static_cast<const GT*>(a.G) + all_n);
     }
     cp_commit();
   };
@@ -385,10 +424,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (++st == kStages) st = 0;
     if (++ahead == kStages) ahead = 0;
     Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
+    const unsigned odd0 = (unsigned)at.b * T + pos;  // its parity is that of the first row's start
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      u[i] = Tl::X::get(tile, i).get();
-      Raw<GT, VC> g = Tl::G::get(tile + Tl::X::kBytes, i);
+      const int half = (int)(odd0 + i) & 1;
+      u[i] = Tl::X::get(tile, i, half).get();
+      Raw<GT, VC> g = Tl::G::get(tile + Tl::X::kBytes, i, half);
       if constexpr (SIG) {
         g.hold();
         V na;
@@ -420,14 +461,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         h = fma(av[i], h, u[i]);
-        Raw<E, VC>::store(rows(out, i, D), h);
+        put<E, VC, ODD>(rows(out, i, D), h, at.two);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i < n) {
           h = pick(rs >> i & 1, u[i], fma(av[i], h, u[i]));
-          Raw<E, VC>::store(rows(out, i, D), h);
+          put<E, VC, ODD>(rows(out, i, D), h, at.two);
         }
     }
   }
@@ -439,26 +480,27 @@ __global__ void __launch_bounds__(kThreads, 2)
 //   D_t = dH_t + c_{t+1},  c_t = a_t D_t  (0 at a document's first token),
 // a recurrence in c of the same form, walked from the last token. The decays stay in registers
 // between the two passes over a run; the other inputs are read from shared memory again.
-template <typename E, typename GT, bool SIG, int VC, int R, int CB>
+template <typename E, typename GT, bool SIG, int VC, int R, int CB, bool ODD>
 struct BwdTiles {
-  using X = RowTile<E, VC, R, CB>;
-  using G = RowTile<GT, VC, R, sizeof(GT) == 4 && CB < 4 ? 4 : CB>;
+  using X = RowTile<E, VC, R, CB, ODD>;
+  using G = RowTile<GT, VC, R, CB, ODD>;
   static constexpr int oD = G::kBytes, oH = oD + X::kBytes, oX = oH + X::kBytes;
   static constexpr int kStage = oX + (SIG ? X::kBytes : 0);  // of one warp
-  static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage;
+  static constexpr size_t kSmem = (size_t)kWarps * kStagesOf<ODD> * kStage;
 };
-template <typename E, typename GT, bool SIG, int VC, int R, int CB>
+template <typename E, typename GT, bool SIG, int VC, int R, int CB, bool ODD>
 __global__ void __launch_bounds__(kThreads, 2)
     recur_bwd_kernel(const __grid_constant__ RecurArgs a, const int cluster) {
   using V = Vec<VC>;
-  using Tl = BwdTiles<E, GT, SIG, VC, R, CB>;
+  using Tl = BwdTiles<E, GT, SIG, VC, R, CB, ODD>;
+  constexpr int kStages = kStagesOf<ODD>;
   extern __shared__ __align__(16) uint8_t tiles[];
   __shared__ Joins<VC> js;
   const Place<VC> at(a, cluster);
   const unsigned T = a.T, D = a.D, stride = (unsigned)at.cl * kWarps * R;
   const int w = threadIdx.x >> 5;
   uint8_t* mine = tiles + w * kStages * Tl::kStage;
-  const size_t base = (size_t)at.b * T * D + at.c0;
+  const size_t base = (size_t)at.b * T * D + at.c0, all_n = (size_t)a.B * T * D;
   const E* X = static_cast<const E*>(a.X) + base;
   const GT* G = static_cast<const GT*>(a.G) + base;
   const E* H = static_cast<const E*>(a.H_in) + base;
@@ -472,10 +514,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int n = min(T - p, (unsigned)R), nh = min(T - 1 - p, (unsigned)R), width = a.D - at.c0;
       const uint32_t dst = smem_u32(mine) + st * Tl::kStage;
       const size_t o = (size_t)(T - 1 - p) * D;
-      Tl::G::template fetch<true>(dst, G + o, D, n, width);
-      Tl::X::template fetch<true>(dst + Tl::oD, dH + o, D, n, width);
-      if (nh > 0) Tl::X::template fetch<true>(dst + Tl::oH, H + o - D, D, nh, width);
-      if constexpr (SIG) Tl::X::template fetch<true>(dst + Tl::oX, X + o, D, n, width);
+      Tl::G::template fetch<true>(dst, G + o, D, n, width, static_cast<const GT*>(a.G) + all_n);
+      Tl::X::template fetch<true>(dst + Tl::oD, dH + o, D, n, width, static_cast<const E*>(a.dH) + all_n);
+      if (nh > 0)
+        Tl::X::template fetch<true>(dst + Tl::oH, H + o - D, D, nh, width, static_cast<const E*>(a.H_in) + all_n);
+      if constexpr (SIG)
+        Tl::X::template fetch<true>(dst + Tl::oX, X + o, D, n, width, static_cast<const E*>(a.X) + all_n);
     }
     cp_commit();
   };
@@ -504,9 +548,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (++st == kStages) st = 0;
     if (++ahead == kStages) ahead = 0;
     Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
+    const unsigned odd0 = (unsigned)at.b * T + T - 1 - pos;  // parity of the first row's start
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      Raw<GT, VC> g = Tl::G::get(tile, i);
+      Raw<GT, VC> g = Tl::G::get(tile, i, (int)(odd0 + i) & 1);
       if constexpr (SIG) {
         g.hold();
         gate_of(g.get(), av[i], na[i]);
@@ -519,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         m.A = mul(m.A, av[i]);
-        m.U = mul(av[i], add(Tl::X::get(tile + Tl::oD, i).get(), m.U));
+        m.U = mul(av[i], add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), m.U));
       }
     } else {
 #pragma unroll
@@ -527,30 +572,30 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (i < n) {
           m.A = mul(m.A, av[i]);
           m.U = pick(rs >> i & 1, all<VC>(0.f),
-                     mul(av[i], add(Tl::X::get(tile + Tl::oD, i).get(), m.U)));
+                     mul(av[i], add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), m.U)));
         }
     }
     V c = join_runs(js, round, at.cl, at.rank, m, rs != 0, carry, a.err);
     if (!at.ok || n == 0) continue;
     const size_t o = (size_t)(T - 1 - pos) * D;
     auto token = [&](int i, V prev, bool first) {
-      const V Dt = add(Tl::X::get(tile + Tl::oD, i).get(), c);
+      const V Dt = add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), c);
       c = mul(av[i], Dt);
       V x = Dt, g;
       if constexpr (SIG) {
         x = mul(na[i], Dt);
         // D_t (h_{t-1} - x) a (1 - a)
-        g = mul(mul(c, na[i]), fma(Tl::X::get(tile + Tl::oX, i).get(), all<VC>(-1.f), prev));
+        g = mul(mul(c, na[i]), fma(Tl::X::get(tile + Tl::oX, i, (int)(odd0 + i) & 1).get(), all<VC>(-1.f), prev));
       } else {
         g = first ? all<VC>(0.f) : mul(Dt, prev);
       }
       if (first) c = all<VC>(0.f);
-      Raw<E, VC>::store(rows_back(dX + o, i, D), x);
-      Raw<GT, VC>::store(rows_back(dG + o, i, D), g);
+      put<E, VC, ODD>(rows_back(dX + o, i, D), x, at.two);
+      put<GT, VC, ODD>(rows_back(dG + o, i, D), g, at.two);
     };
     if (plain) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) token(i, Tl::X::get(tile + Tl::oH, i).get(), false);
+      for (int i = 0; i < R; ++i) token(i, Tl::X::get(tile + Tl::oH, i, (int)(odd0 + i + 1) & 1).get(), false);
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
@@ -559,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           V prev = all<VC>(0.f);
           if (!first) {
             if (pos + i == T - 1) prev = load_state<VC>(a.h0, a, at);
-            else prev = Tl::X::get(tile + Tl::oH, i).get();
+            else prev = Tl::X::get(tile + Tl::oH, i, (int)(odd0 + i + 1) & 1).get();
           }
           token(i, prev, first);
         }
@@ -667,42 +712,35 @@ cudaError_t launch(K kernel, size_t smem, const RecurArgs& a, int vc, int run, c
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-#ifndef RF
-#define RF 16
-#define RB 8
-#define R1F 16
-#define R1B 8
-#endif
-template <typename E, typename GT, bool SIG, int VC, int CB>
+template <typename E, typename GT, bool SIG, int VC, int CB, bool ODD>
 cudaError_t fwd(const RecurArgs& a, cudaStream_t s) {
-  constexpr int R = sizeof(GT) * VC == 8 ? RF / 2 : VC == 2 ? RF : R1F;
-  return launch(recur_fwd_kernel<E, GT, SIG, VC, R, CB>, FwdTiles<E, GT, VC, R, CB>::kSmem, a, VC, R, s);
+  constexpr int R = sizeof(GT) * VC == 8 ? 8 : 16;  // what a stage of shared memory has room for
+  return launch(recur_fwd_kernel<E, GT, SIG, VC, R, CB, ODD>, FwdTiles<E, GT, VC, R, CB, ODD>::kSmem, a, VC, R, s);
 }
-template <typename E, typename GT, bool SIG, int VC, int CB>
+template <typename E, typename GT, bool SIG, int VC, int CB, bool ODD>
 cudaError_t bwd(const RecurArgs& a, cudaStream_t s) {
-  constexpr int R = VC == 2 ? RB : R1B;
-  return launch(recur_bwd_kernel<E, GT, SIG, VC, R, CB>, BwdTiles<E, GT, SIG, VC, R, CB>::kSmem, a, VC, R, s);
+  constexpr int R = 8;
+  return launch(recur_bwd_kernel<E, GT, SIG, VC, R, CB, ODD>, BwdTiles<E, GT, SIG, VC, R, CB, ODD>::kSmem, a, VC, R, s);
 }
 
 }  // namespace
 
-// bf16 takes two features a thread where rows start on a pair's boundary; copies are of 16 bytes
-// where rows do.
-#define RECUR_DISPATCH(f)                                                       \
-  do {                                                                          \
-    if (a.bf16 && a.sigmoid)                                                    \
-      return a.D % 8 == 0   ? f<bf16, bf16, true, 2, 16>(a, s)                  \
-             : a.D % 2 == 0 ? f<bf16, bf16, true, 2, 4>(a, s)                   \
-                            : f<bf16, bf16, true, 1, 2>(a, s);                  \
-    if (a.bf16)                                                                 \
-      return a.D % 8 == 0   ? f<bf16, float, false, 2, 16>(a, s)                \
-             : a.D % 2 == 0 ? f<bf16, float, false, 2, 4>(a, s)                 \
-                            : f<bf16, float, false, 1, 2>(a, s);                \
-    if (a.sigmoid)                                                              \
-      return a.D % 4 == 0 ? f<float, float, true, 1, 16>(a, s)                  \
-                          : f<float, float, true, 1, 4>(a, s);                  \
-    return a.D % 4 == 0 ? f<float, float, false, 1, 16>(a, s)                   \
-                        : f<float, float, false, 1, 4>(a, s);                   \
+// bf16 takes two features a thread; copies are of 16 bytes where all rows start on such a boundary.
+#define RECUR_DISPATCH(f)                                                \
+  do {                                                                   \
+    if (a.bf16 && a.sigmoid)                                             \
+      return a.D % 8 == 0   ? f<bf16, bf16, true, 2, 16, false>(a, s)    \
+             : a.D % 2 == 0 ? f<bf16, bf16, true, 2, 4, false>(a, s)     \
+                            : f<bf16, bf16, true, 2, 4, true>(a, s);     \
+    if (a.bf16)                                                          \
+      return a.D % 8 == 0   ? f<bf16, float, false, 2, 16, false>(a, s)  \
+             : a.D % 2 == 0 ? f<bf16, float, false, 2, 4, false>(a, s)   \
+                            : f<bf16, float, false, 2, 4, true>(a, s);   \
+    if (a.sigmoid)                                                       \
+      return a.D % 4 == 0 ? f<float, float, true, 1, 16, false>(a, s)    \
+                          : f<float, float, true, 1, 4, false>(a, s);    \
+    return a.D % 4 == 0 ? f<float, float, false, 1, 16, false>(a, s)     \
+                        : f<float, float, false, 1, 4, false>(a, s);     \
   } while (0)
 
 cudaError_t recur_fwd(const RecurArgs& a, cudaStream_t s) { RECUR_DISPATCH(fwd); }

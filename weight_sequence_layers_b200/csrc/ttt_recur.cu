@@ -190,7 +190,7 @@ __device__ __forceinline__ Vec<VC> fold(const Map<VC> (*maps)[32], int lo, int h
                                         Vec<VC> h) {
   const Map<VC>* m = &maps[0][threadIdx.x & 31];
   if (resets == 0) {
-#pragma unroll 2
+#pragma unroll 4
     for (int s = lo; s < hi; ++s) h = fma(m[s * 32].A, h, m[s * 32].U);
   } else {
     for (int s = lo; s < hi; ++s) h = pick(resets >> s & 1, m[s * 32].U, fma(m[s * 32].A, h, m[s * 32].U));
@@ -220,20 +220,30 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
     carry = fold<VC>(js.seg[buf], w, kWarps, rs, in);
     return in;
   }
-  if (w < cl) {  // warp w hands the CTA's map to CTA w
-    Map<VC> c{all<VC>(1.f), fold<VC>(js.seg[buf], 0, kWarps, rs, all<VC>(0.f))};
-#pragma unroll 2
-    for (int s = 0; s < kWarps; ++s) c.A = mul(c.A, js.seg[buf][s][lane].A);
-    const uint32_t bar = peer_addr(full, w);
-    st_async(peer_addr(smem_u32(&js.cta[buf][rank][lane]), w), c, bar);
-    if (lane == 0) st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), w), rs, bar);
+  // the map of the runs before this warp's; the last warp hands the CTA's to all CTAs
+  Map<VC> ex{all<VC>(1.f), all<VC>(0.f)};
+  const Map<VC>* seg = &js.seg[buf][0][lane];
+#pragma unroll 4
+  for (int s = 0; s < w; ++s) {
+    const Map<VC> q = seg[s * 32];
+    ex.A = mul(ex.A, q.A);
+    ex.U = fma(q.A, ex.U, q.U);
+    if (rs >> s & 1) ex.U = q.U;
+  }
+  if (w == kWarps - 1) {
+    const Map<VC> c{mul(ex.A, m.A), pick(reset, m.U, fma(m.A, ex.U, m.U))};
+    for (int r = 0; r < cl; ++r) {
+      const uint32_t bar = peer_addr(full, r);
+      st_async(peer_addr(smem_u32(&js.cta[buf][rank][lane]), r), c, bar);
+      if (lane == 0) st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), r), rs, bar);
+    }
   }
   // a wait that runs out is recorded, and the rounds go on without waiting
   mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
   const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][lane & (kMaxCluster - 1)]);
   const Vec<VC> in = fold<VC>(js.cta[buf], 0, rank, crs, carry);
   carry = fold<VC>(js.cta[buf], rank, cl, crs, in);
-  return fold<VC>(js.seg[buf], 0, w, rs, in);
+  return pick(rs & ((1u << w) - 1), ex.U, fma(ex.A, in, ex.U));
 }
 
 // This thread's place: features c.. of batch row b, run w of CTA `rank` of the cluster.
@@ -674,9 +684,9 @@ __global__ void __launch_bounds__(kStepThreads) recur_step_kernel(const __grid_c
 
 // ------------------------------------------------------------------------------------ launch
 // CTAs along the sequence. A cluster lies within one GPC, so that fewer CTAs than two per SM are
-// resident with the larger sizes (kResident, measured with the occupancy query). The choice is
-// the smallest count of rounds over all waves of the grid, with two rounds more per wave for its
-// start and end.
+// resident with the larger sizes (kResident, from the occupancy query). The choice is the least
+// time by the measured times of a round, with two rounds more per wave for its start and end
+// (32768 x 2560 forward: 407 us with 1, 188 with 3, 139 with 6, 199 with 8).
 int cluster_of(const RecurArgs& a, long long ctas, int run) {
   constexpr int kResident[kMaxCluster + 1] = {0, 296, 296, 279, 284, 280, 270, 259, 264};
   int best = 1;
@@ -684,7 +694,10 @@ int cluster_of(const RecurArgs& a, long long ctas, int run) {
   for (int cl = 1; cl <= kMaxCluster; ++cl) {
     if (cl > 1 && (long long)(cl - 1) * kWarps * run >= a.T) break;  // CTAs without a token
     const long long waves = (ctas * cl + kResident[cl] - 1) / kResident[cl];
-    const long long tile = (long long)cl * kWarps * run, cost = waves * ((a.T + tile - 1) / tile + 2);
+    const long long tile = (long long)cl * kWarps * run, rounds = (a.T + tile - 1) / tile;
+    // tenths of a microsecond: a round of a CTA alone on its SM, the join of a cluster, a second CTA
+    const long long round = 15 + (cl > 1 ? 6 : 0) + (ctas * cl > kResident[1] / 2 ? 10 : 0);
+    const long long cost = waves * (rounds + 2) * round;
     if (cl == 1 || cost < least) best = cl, least = cost;
   }
   return best;

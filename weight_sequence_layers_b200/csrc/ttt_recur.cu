@@ -145,27 +145,25 @@ __device__ __forceinline__ E* rows_back(E* p, int i, unsigned D) {
 }
 
 // ------------------------------------------------------------------------------------- joins
+// A CTA's runs and a cluster's CTAs are joined by scans over eight lanes: in warp w, lane 8 q + s
+// takes the maps s (of run s, or of CTA s) of features kScan w + q + 4 k, k < VC, so that a scan
+// is three shuffles deep and all warps share the work.
 template <int VC>
-struct __align__(8 * VC) Map {
-  Vec<VC> A, U;
-};
-template <int VC>
-struct Joins {  // two buffers in turn: a buffer is written again two joins later
-  Map<VC> seg[2][kWarps][32], cta[2][kMaxCluster][32];
-  unsigned seg_reset[2][kWarps], cta_reset[2][kMaxCluster];
+struct Joins {
+  static constexpr int kCols = 32 * VC, kScan = kCols / kWarps;
+  static constexpr int kPitch = kCols + 4;  // rows of neighbouring s fall into different banks
+  float A[kWarps][kPitch], U[kWarps][kPitch];  // the runs' maps
+  float in[kWarps][kPitch];                    // the states that enter the runs
+  float2 cta[2][kMaxCluster][kPitch];          // the CTAs' maps, two rounds in turn
+  unsigned run_reset[kWarps], cta_reset[2][kMaxCluster];
   uint64_t full[2];  // the cluster's maps of the round have arrived in cta and cta_reset
   int abort_flag;
 };
 // Stores to a CTA of the cluster that count their bytes on its barrier: the receiver waits for
 // the data alone, where a release would make every round wait for the outputs' stores too.
-__device__ __forceinline__ void st_async(uint32_t addr, const Map<1>& m, uint32_t bar) {
+__device__ __forceinline__ void st_async(uint32_t addr, float a, float u, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1,%2}, [%3];"
-               ::"r"(addr), "f"(m.A), "f"(m.U), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void st_async(uint32_t addr, const Map<2>& m, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], "
-               "{%1,%2,%3,%4}, [%5];" ::"r"(addr), "f"(m.A.x), "f"(m.A.y), "f"(m.U.x), "f"(m.U.y),
-               "r"(bar) : "memory");
+               ::"r"(addr), "f"(a), "f"(u), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];"
@@ -184,66 +182,81 @@ __device__ __forceinline__ void join_init(Joins<VC>& js, int cl) {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// h through maps lo..hi-1 in order (lo and hi uniform over the warp). resets: bit s for map s.
-template <int VC>
-__device__ __forceinline__ Vec<VC> fold(const Map<VC> (*maps)[32], int lo, int hi, unsigned resets,
-                                        Vec<VC> h) {
-  const Map<VC>* m = &maps[0][threadIdx.x & 31];
-  if (resets == 0) {
-#pragma unroll 4
-    for (int s = lo; s < hi; ++s) h = fma(m[s * 32].A, h, m[s * 32].U);
-  } else {
-    for (int s = lo; s < hi; ++s) h = pick(resets >> s & 1, m[s * 32].U, fma(m[s * 32].A, h, m[s * 32].U));
-  }
-  return h;
-}
-
-// Joins the warps' maps m (reset: it holds a document's first token) of one round: `carry` goes
-// from the state that enters the round to the one that leaves it; returns the state that enters
-// this warp's run. All threads of the cluster call it the same number of times.
-// A buffer of `cta` is free again when the next round's maps arrive: a CTA sends those behind
-// the barrier that all its threads reach after reading it, and sends into the buffer again only
-// after it has them from all.
-template <int VC>
-__device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int cl, int rank,
-                                             const Map<VC>& m, bool reset, Vec<VC>& carry,
-                                             unsigned* err) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = round & 1;
-  js.seg[buf][w][lane] = m;
-  if (lane == 0) js.seg_reset[buf][w] = reset;
-  const uint32_t full = smem_u32(&js.full[buf]);
-  if (cl > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(full, cl * (32 * sizeof(Map<VC>) + 4));
-  __syncthreads();
-  const unsigned rs = __ballot_sync(~0u, lane < kWarps && js.seg_reset[buf][lane & (kWarps - 1)]);
-  if (cl == 1) {
-    const Vec<VC> in = fold<VC>(js.seg[buf], 0, w, rs, carry);
-    carry = fold<VC>(js.seg[buf], w, kWarps, rs, in);
-    return in;
-  }
-  // the map of the runs before this warp's; the last warp hands the CTA's to all CTAs
-  Map<VC> ex{all<VC>(1.f), all<VC>(0.f)};
-  const Map<VC>* seg = &js.seg[buf][0][lane];
-#pragma unroll 4
-  for (int s = 0; s < w; ++s) {
-    const Map<VC> q = seg[s * 32];
-    ex.A = mul(ex.A, q.A);
-    ex.U = fma(q.A, ex.U, q.U);
-    if (rs >> s & 1) ex.U = q.U;
-  }
-  if (w == kWarps - 1) {
-    const Map<VC> c{mul(ex.A, m.A), pick(reset, m.U, fma(m.A, ex.U, m.U))};
-    for (int r = 0; r < cl; ++r) {
-      const uint32_t bar = peer_addr(full, r);
-      st_async(peer_addr(smem_u32(&js.cta[buf][rank][lane]), r), c, bar);
-      if (lane == 0) st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), r), rs, bar);
+// Inclusive scan of the maps of lanes s = 0..7 of each group: afterwards lane s holds map s after
+// ... after map 0. resets: bit s for map s; a map that holds a reset does not see what is before.
+__device__ __forceinline__ void scan8(float& A, float& U, unsigned resets) {
+  const int s = threadIdx.x & 7;
+#pragma unroll
+  for (int o = 1; o < 8; o *= 2) {
+    const float a = __shfl_up_sync(~0u, A, o, 8), u = __shfl_up_sync(~0u, U, o, 8);
+    // maps s - o + 1 .. s are in (A, U)
+    if (s >= o) {
+      if ((resets >> (s - o + 1) & ((1u << o) - 1)) == 0) U = fmaf(A, u, U);
+      A *= a;
     }
   }
-  // a wait that runs out is recorded, and the rounds go on without waiting
-  mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
-  const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][lane & (kMaxCluster - 1)]);
-  const Vec<VC> in = fold<VC>(js.cta[buf], 0, rank, crs, carry);
-  carry = fold<VC>(js.cta[buf], rank, cl, crs, in);
-  return pick(rs & ((1u << w) - 1), ex.U, fma(ex.A, in, ex.U));
+}
+
+// Joins the runs' maps (A, U) (reset: the run holds a document's first token) of one round:
+// carry goes from the state that enters the round to the one that leaves it (in the layout of the
+// scans); returns the state that enters this warp's run. All threads of the cluster call it the
+// same number of times. A buffer of `cta` is free again when the next round's maps arrive: a CTA
+// sends those behind a barrier that all its threads reach after reading it, and sends into the
+// buffer again only after it has them from all.
+template <int VC>
+__device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int cl, int rank,
+                                             Vec<VC> A, Vec<VC> U, bool reset, float (&carry)[VC],
+                                             unsigned* err) {
+  using J = Joins<VC>;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = round & 1;
+  const int s = lane & 7, col = w * J::kScan + (lane >> 3);
+  *reinterpret_cast<Vec<VC>*>(&js.A[w][lane * VC]) = A;
+  *reinterpret_cast<Vec<VC>*>(&js.U[w][lane * VC]) = U;
+  if (lane == 0) js.run_reset[w] = reset;
+  const uint32_t full = smem_u32(&js.full[buf]);
+  if (cl > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(full, cl * (J::kCols * 8 + 4));
+  __syncthreads();
+  const unsigned rs = __ballot_sync(~0u, lane < kWarps && js.run_reset[s]);
+  float a[VC], u[VC], in[VC];
+#pragma unroll
+  for (int k = 0; k < VC; ++k) {
+    a[k] = js.A[s][col + 4 * k];
+    u[k] = js.U[s][col + 4 * k];
+    scan8(a[k], u[k], rs);
+    in[k] = carry[k];
+  }
+  if (cl > 1) {
+    const uint32_t bar = peer_addr(full, s < cl ? s : 0);  // lane s of a group sends to CTA s
+#pragma unroll
+    for (int k = 0; k < VC; ++k) {
+      const float ta = __shfl_sync(~0u, a[k], 7, 8), tu = __shfl_sync(~0u, u[k], 7, 8);
+      if (s < cl) st_async(peer_addr(smem_u32(&js.cta[buf][rank][col + 4 * k]), s), ta, tu, bar);
+    }
+    if (w == 0 && lane < cl) st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), lane), rs, bar);
+    // a wait that runs out is recorded, and the rounds go on without waiting
+    mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
+    __syncwarp();
+    const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][s]);
+#pragma unroll
+    for (int k = 0; k < VC; ++k) {
+      const float2 q = js.cta[buf][s][col + 4 * k];
+      float ca = s < cl ? q.x : 1.f, cu = s < cl ? q.y : 0.f;
+      scan8(ca, cu, crs);
+      const float h = (crs & ((2u << s) - 1)) ? cu : fmaf(ca, carry[k], cu);  // after CTA s
+      const float before = __shfl_sync(~0u, h, rank - 1, 8);
+      in[k] = rank == 0 ? carry[k] : before;
+      carry[k] = __shfl_sync(~0u, h, 7, 8);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < VC; ++k) {
+    const float h = (rs & ((2u << s) - 1)) ? u[k] : fmaf(a[k], in[k], u[k]);  // after run s
+    const float before = __shfl_up_sync(~0u, h, 1, 8);
+    js.in[s][col + 4 * k] = s == 0 ? in[k] : before;
+    if (cl == 1) carry[k] = __shfl_sync(~0u, h, 7, 8);
+  }
+  __syncthreads();
+  return *reinterpret_cast<const Vec<VC>*>(&js.in[w][lane * VC]);
 }
 
 // This thread's place: features c.. of batch row b, run w of CTA `rank` of the cluster.
@@ -280,11 +293,22 @@ __device__ __forceinline__ void put(E* p, Vec<VC> v, bool two) {
     Raw<E, VC>::store(p, v);
   }
 }
+// The state in the layout of the scans.
 template <int VC>
-__device__ __forceinline__ void store_state(float* p, const RecurArgs& a, const Place<VC>& at,
-                                            Vec<VC> v) {
-  if (p && at.ok && at.rank == 0 && threadIdx.x < 32)
-    put<float, VC, true>(p + (size_t)at.b * a.D + at.c, v, at.two);
+__device__ __forceinline__ void load_carry(const float* p, const RecurArgs& a, const Place<VC>& at,
+                                           float (&v)[VC]) {
+  const int c = at.c0 + (threadIdx.x >> 5) * Joins<VC>::kScan + (threadIdx.x >> 3 & 3);
+#pragma unroll
+  for (int k = 0; k < VC; ++k) v[k] = p && c + 4 * k < a.D ? p[(size_t)at.b * a.D + c + 4 * k] : 0.f;
+}
+template <int VC>
+__device__ __forceinline__ void store_carry(float* p, const RecurArgs& a, const Place<VC>& at,
+                                            const float (&v)[VC]) {
+  const int c = at.c0 + (threadIdx.x >> 5) * Joins<VC>::kScan + (threadIdx.x >> 3 & 3);
+  if (p && at.rank == 0 && (threadIdx.x & 7) == 0)
+#pragma unroll
+    for (int k = 0; k < VC; ++k)
+      if (c + 4 * k < a.D) p[(size_t)at.b * a.D + c + 4 * k] = v[k];
 }
 // The documents' marks of R positions from pos of a walk (position p is token p, or T - 1 - p
 // with REV): lane i loads that of position pos + i.
@@ -418,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     mark[k] = load_reset<R, false>(a, at.b, pos + k * stride);
   }
   join_init(js, at.cl);
-  V carry = load_state<VC>(a.h0, a, at);
+  float carry[VC];
+  load_carry(a.h0, a, at, carry);
   int st = 0, ahead = kStages - 1;
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
     V av[R], u[R];
@@ -433,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint8_t* tile = mine + st * Tl::kStage;
     if (++st == kStages) st = 0;
     if (++ahead == kStages) ahead = 0;
-    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
+    V mA = all<VC>(1.f), mU = all<VC>(0.f);
     const unsigned odd0 = (unsigned)at.b * T + pos;  // its parity is that of the first row's start
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -453,18 +478,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (rs == 0 && n == R) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        m.A = mul(m.A, av[i]);
-        m.U = fma(av[i], m.U, u[i]);
+        mA = mul(mA, av[i]);
+        mU = fma(av[i], mU, u[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i < n) {
-          m.A = mul(m.A, av[i]);
-          m.U = pick(rs >> i & 1, u[i], fma(av[i], m.U, u[i]));
+          mA = mul(mA, av[i]);
+          mU = pick(rs >> i & 1, u[i], fma(av[i], mU, u[i]));
         }
     }
-    V h = join_runs(js, round, at.cl, at.rank, m, rs != 0, carry, a.err);
+    V h = join_runs(js, round, at.cl, at.rank, mA, mU, rs != 0, carry, a.err);
     if (!at.ok) continue;
     E* out = H + (size_t)pos * D;
     if (rs == 0 && n == R) {
@@ -482,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
   }
-  store_state<VC>(a.h_final, a, at, carry);
+  store_carry(a.h_final, a, at, carry);
 }
 
 // ---------------------------------------------------------------------------------- backward
@@ -541,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     mark[k] = load_reset<R, true>(a, at.b, pos + k * stride);
   }
   join_init(js, at.cl);
-  V carry = load_state<VC>(a.dh_final, a, at);
+  float carry[VC];
+  load_carry(a.dh_final, a, at, carry);
   int st = 0, ahead = kStages - 1;
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
     V av[R], na[SIG ? R : 1];
@@ -557,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint8_t* tile = mine + st * Tl::kStage;
     if (++st == kStages) st = 0;
     if (++ahead == kStages) ahead = 0;
-    Map<VC> m{all<VC>(1.f), all<VC>(0.f)};
+    V mA = all<VC>(1.f), mU = all<VC>(0.f);
     const unsigned odd0 = (unsigned)at.b * T + T - 1 - pos;  // parity of the first row's start
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -573,19 +599,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (plain) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        m.A = mul(m.A, av[i]);
-        m.U = mul(av[i], add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), m.U));
+        mA = mul(mA, av[i]);
+        mU = mul(av[i], add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), mU));
       }
     } else {
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i < n) {
-          m.A = mul(m.A, av[i]);
-          m.U = pick(rs >> i & 1, all<VC>(0.f),
-                     mul(av[i], add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), m.U)));
+          mA = mul(mA, av[i]);
+          mU = pick(rs >> i & 1, all<VC>(0.f),
+                     mul(av[i], add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), mU)));
         }
     }
-    V c = join_runs(js, round, at.cl, at.rank, m, rs != 0, carry, a.err);
+    V c = join_runs(js, round, at.cl, at.rank, mA, mU, rs != 0, carry, a.err);
     if (!at.ok || n == 0) continue;
     const size_t o = (size_t)(T - 1 - pos) * D;
     auto token = [&](int i, V prev, bool first) {
@@ -620,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
   }
-  store_state<VC>(a.dh0, a, at, carry);
+  store_carry(a.dh0, a, at, carry);
 }
 
 // -------------------------------------------------------------------------------------- step

@@ -184,15 +184,23 @@ __device__ __forceinline__ void join_init(Joins<VC>& js, int cl) {
 }
 // Inclusive scan of the maps of lanes s = 0..7 of each group: afterwards lane s holds map s after
 // ... after map 0. resets: bit s for map s; a map that holds a reset does not see what is before.
-__device__ __forceinline__ void scan8(float& A, float& U, unsigned resets) {
+template <int VC>
+__device__ __forceinline__ void scan8(float (&A)[VC], float (&U)[VC], unsigned resets) {
   const int s = threadIdx.x & 7;
 #pragma unroll
   for (int o = 1; o < 8; o *= 2) {
-    const float a = __shfl_up_sync(~0u, A, o, 8), u = __shfl_up_sync(~0u, U, o, 8);
-    // maps s - o + 1 .. s are in (A, U)
-    if (s >= o) {
-      if ((resets >> (s - o + 1) & ((1u << o) - 1)) == 0) U = fmaf(A, u, U);
-      A *= a;
+    float a[VC], u[VC];
+#pragma unroll
+    for (int k = 0; k < VC; ++k) {
+      a[k] = __shfl_up_sync(~0u, A[k], o, 8);
+      u[k] = __shfl_up_sync(~0u, U[k], o, 8);
+    }
+    // maps s - o + 1 .. s are in (A, U); lanes without a map before theirs keep them
+    const bool in = s >= o, see = in && (resets >> (s - o + 1) & ((1u << o) - 1)) == 0;
+#pragma unroll
+    for (int k = 0; k < VC; ++k) {
+      U[k] = see ? fmaf(A[k], u[k], U[k]) : U[k];
+      A[k] = in ? A[k] * a[k] : A[k];
     }
   }
 }
@@ -222,9 +230,9 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
   for (int k = 0; k < VC; ++k) {
     a[k] = js.A[s][col + 4 * k];
     u[k] = js.U[s][col + 4 * k];
-    scan8(a[k], u[k], rs);
     in[k] = carry[k];
   }
+  scan8(a, u, rs);
   if (cl > 1) {
     const uint32_t bar = peer_addr(full, s < cl ? s : 0);  // lane s of a group sends to CTA s
 #pragma unroll
@@ -237,12 +245,17 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
     mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
     __syncwarp();
     const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][s]);
+    float ca[VC], cu[VC];
 #pragma unroll
     for (int k = 0; k < VC; ++k) {
       const float2 q = js.cta[buf][s][col + 4 * k];
-      float ca = s < cl ? q.x : 1.f, cu = s < cl ? q.y : 0.f;
-      scan8(ca, cu, crs);
-      const float h = (crs & ((2u << s) - 1)) ? cu : fmaf(ca, carry[k], cu);  // after CTA s
+      ca[k] = s < cl ? q.x : 1.f;
+      cu[k] = s < cl ? q.y : 0.f;
+    }
+    scan8(ca, cu, crs);
+#pragma unroll
+    for (int k = 0; k < VC; ++k) {
+      const float h = (crs & ((2u << s) - 1)) ? cu[k] : fmaf(ca[k], carry[k], cu[k]);  // after CTA s
       const float before = __shfl_sync(~0u, h, rank - 1, 8);
       in[k] = rank == 0 ? carry[k] : before;
       carry[k] = __shfl_sync(~0u, h, 7, 8);

@@ -27,13 +27,14 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kSMs = 148;
 constexpr int kNarrowThreads = 128;  // CTA of the narrow-row kernels
-constexpr int kNarrowCtas = 4;       // of them on an SM, by registers
-// Threads of the wide-row kernels on an SM, by the floats of a row that a thread holds.
+// Of them on an SM, and the threads of the wide-row kernels on an SM, by the floats of a row that
+// a thread holds: what the registers leave room for.
+constexpr int narrow_ctas(int floats) { return floats < 16 ? 4 : 3; }
 constexpr int fwd_threads(int floats) { return floats <= 8 ? 1024 : 512; }
 constexpr int bwd_threads(int floats) { return floats <= 8 ? 640 : 512; }
 
-// VEC elements of a row: one 16-byte access, or one element where the width does not keep rows
-// on 16-byte boundaries. Coherent loads, since S may be X or residual and dX may be dS.
+// VEC elements of a row: one 16-byte access; where the width does not keep rows on 16-byte
+// boundaries, a pair for even widths and one element for odd ones. Coherent loads, since S may be X or residual and dX may be dS.
 template <typename E, int VEC>
 struct Pack;
 template <>
@@ -70,6 +71,26 @@ struct Pack<float, 4> {
   static __device__ __forceinline__ void store(float* p, const float2* v) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
   }
+};
+template <>
+struct Pack<bf16, 2> {
+  uint32_t r;
+  __device__ __forceinline__ void load(const bf16* p) {
+    asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+  }
+  __device__ __forceinline__ void get(float2* v) const { v[0] = make_float2(bf16lo(r), bf16hi(r)); }
+  static __device__ __forceinline__ void store(bf16* p, const float2* v) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0].x, v[0].y);
+  }
+};
+template <>
+struct Pack<float, 2> {
+  float2 r;
+  __device__ __forceinline__ void load(const float* p) {
+    asm volatile("ld.global.L1::no_allocate.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "l"(p) : "memory");
+  }
+  __device__ __forceinline__ void get(float2* v) const { v[0] = r; }
+  static __device__ __forceinline__ void store(float* p, const float2* v) { *reinterpret_cast<float2*>(p) = v[0]; }
 };
 template <typename E>
 struct Pack<E, 1> {
@@ -239,7 +260,7 @@ __device__ __forceinline__ void lanes_sum(float (&v)[N]) {
 // loaded ahead while RU are reduced, which keeps enough bytes in flight. RES: with a residual,
 // which doubles a row's bytes.
 template <typename E, int VEC, int NV, int G, int RU, bool RES>
-__global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
+__global__ void __launch_bounds__(kNarrowThreads, narrow_ctas(NV * VEC))
     norm_fwd_narrow(const __grid_constant__ NormArgs a, const Split sp) {
   using F = Frag<E, VEC, NV>;
   constexpr int NG = kNarrowThreads / G, STEP = RU * NG;
@@ -324,7 +345,7 @@ struct Partials {
 };
 
 template <typename E, int VEC, int NV, int G, int RU>
-__global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
+__global__ void __launch_bounds__(kNarrowThreads, narrow_ctas(NV * VEC))
     norm_bwd_narrow(const __grid_constant__ NormArgs a, const Split sp, const Partials pt) {
   using F = Frag<E, VEC, NV>;
   constexpr int NG = kNarrowThreads / G, STEP = RU * NG;
@@ -427,7 +448,7 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowCtas)
 // that one thread issues several rows ahead, so that the bytes in flight cost no registers.
 // A stage is refilled behind the barrier of its row's sum, when all threads hold the row in
 // registers. A bulk copy moves whole 16-byte blocks: where rows start off such a boundary
-// (VEC = 1) the stage holds the blocks around the row and the row starts `off` bytes in; the
+// (VEC of 1 and 2) the stage holds the blocks around the row and the row starts `off` bytes in; the
 // copy never goes past the tensor's last whole block, and the elements behind it (of the last
 // row only) are read directly.
 struct Ring {
@@ -441,7 +462,7 @@ struct RowView {
 // The view of a row that starts at element x of a tensor of `total` elements.
 template <typename E, int VEC>
 __device__ __forceinline__ RowView row_view(size_t x, int d, size_t total) {
-  if (VEC > 1) return {0u, d};
+  if (VEC * sizeof(E) == 16) return {0u, d};
   const size_t b0 = x * sizeof(E), end = total * sizeof(E) & ~(size_t)15;
   const size_t held = end > b0 ? (end - b0) / sizeof(E) : 0;
   return {(uint32_t)(b0 & 15), held < (size_t)d ? (int)held : d};
@@ -450,7 +471,7 @@ __device__ __forceinline__ RowView row_view(size_t x, int d, size_t total) {
 template <typename E, int VEC>
 __device__ __forceinline__ uint32_t row_bytes(size_t x, int d, size_t total) {
   const size_t es = sizeof(E), b0 = x * es;
-  if (VEC > 1) return (uint32_t)(d * es);
+  if (VEC * sizeof(E) == 16) return (uint32_t)(d * es);
   const size_t from = b0 & ~(size_t)15, end = total * es & ~(size_t)15;
   const size_t to = (b0 + d * es + 15) & ~(size_t)15;
   const size_t stop = to < end ? to : end;
@@ -472,8 +493,9 @@ __device__ __forceinline__ void slot_read(const Frag<E, VEC, NV>& f, const uint8
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const E* sp = reinterpret_cast<const E*>(slot + rv.off) + f.at(n);
-    if constexpr (VEC == 1) p[n].r = f.at(n) < rv.in_slot ? *sp : row[f.at(n)];
-    else p[n].r = *reinterpret_cast<const decltype(p[n].r)*>(sp);
+    using R = decltype(p[n].r);
+    const bool held = VEC * sizeof(E) == 16 || f.at(n) < rv.in_slot;
+    p[n].r = held ? *reinterpret_cast<const R*>(sp) : *reinterpret_cast<const R*>(row + f.at(n));
   }
   f.get(p, v);
 }
@@ -782,17 +804,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 struct Shape {
   int vec, nv, g, threads;  // g = 0: a wide row, one CTA of `threads`
 };
-// Narrow rows take as few lanes as hold the row in at most two (scalar: eight) accesses each.
-// Wide rows: the forward takes one access (scalar: four) per thread up to 512 threads, then more.
+// Narrow rows take as few lanes as hold the row in at most two (small accesses: eight,
+// or sixteen single elements) each.
+// Wide rows: the forward takes one access (small ones: four) per thread up to 512 threads, then more.
 // The backward takes 16 values per thread: its work around a row is the same for 8 (32768 x 2560:
 // 110 us against 143 with twice the threads and two rows per barrier).
 Shape shape_of(const NormArgs& a, bool bwd) {
   const int v = a.bf16 ? 8 : 4;
   Shape s;
-  s.vec = a.d % v == 0 ? v : 1;
+  s.vec = a.d % v == 0 ? v : a.d % 2 == 0 ? 2 : 1;
   const int n = a.d / s.vec;
   s.threads = kNarrowThreads;
-  if (s.vec > 1) {
+  if (s.vec == v) {
     if (n <= 8) { s.g = 8; s.nv = 1; return s; }
     if (n <= 16) { s.g = 16; s.nv = 1; return s; }
     if (n <= 32) { s.g = 32; s.nv = 1; return s; }
@@ -801,9 +824,12 @@ Shape shape_of(const NormArgs& a, bool bwd) {
     if (bwd) s.nv = std::max(s.nv, 16 / s.vec);
   } else {
     if (n <= 32) { s.g = 32; s.nv = 1; return s; }
+    if (n <= 64) { s.g = 32; s.nv = 2; return s; }
     if (n <= 128) { s.g = 32; s.nv = 4; return s; }
     if (n <= 256) { s.g = 32; s.nv = 8; return s; }
-    s.nv = n <= 2048 ? 4 : n <= 4096 ? 8 : 32;
+    if (n <= 512 && s.vec == 1) { s.g = 32; s.nv = 16; return s; }
+    s.nv = n <= 2048 ? 4 : n <= 4096 ? 8 : s.vec == 2 ? 16 : 32;
+    if (bwd && s.vec == 2) s.nv = std::max(s.nv, 8);
   }
   s.g = 0;
   s.threads = ((n + s.nv - 1) / s.nv + 31) / 32 * 32;
@@ -812,8 +838,9 @@ Shape shape_of(const NormArgs& a, bool bwd) {
 
 // CTAs of an SM, from the threads that the kernels' registers leave room for.
 int ctas_per_sm(const Shape& sh, bool bwd) {
-  if (sh.g) return kNarrowCtas;
-  const int floats = sh.nv * sh.vec, threads = bwd ? bwd_threads(floats) : fwd_threads(floats);
+  const int floats = sh.nv * sh.vec;
+  if (sh.g) return narrow_ctas(floats);
+  const int threads = bwd ? bwd_threads(floats) : fwd_threads(floats);
   return std::max(1, std::min(8, threads / sh.threads));
 }
 // A run of the backward has at least four rows per group, so that the shares of the weight
@@ -842,7 +869,7 @@ Ring ring_of(const NormArgs& a, const Shape& sh, int nsrc, bool bwd) {
   const uint32_t es = a.bf16 ? 2 : 4;
   Ring r;
   // off a 16-byte boundary a row touches up to one block more on each side
-  r.slot = sh.vec > 1 ? a.d * es : (a.d * es + 30) / 16 * 16;
+  r.slot = sh.vec * es == 16 ? a.d * es : (a.d * es + 30) / 16 * 16;
   const uint32_t room = kRingBytes / ctas_per_sm(sh, bwd) / (nsrc * r.slot);
   r.stages = (int)std::max(1u, std::min((uint32_t)kMaxStages, room));
   return r;
@@ -934,14 +961,21 @@ cudaError_t dispatch_vec(const NormArgs& a, const Shape& sh, cudaStream_t s) {
   if constexpr (VEC == 4) return F::template wide<E, VEC, 8>(a, sh, s);  // float32 rows only
   return cudaErrorInvalidValue;
 }
-template <typename F, typename E>
-cudaError_t dispatch_scalar(const NormArgs& a, const Shape& sh, cudaStream_t s) {
-  if (sh.g == 32 && sh.nv == 1) return F::template narrow<E, 1, 1, 32, 2>(a, sh, s);
-  if (sh.g == 32 && sh.nv == 4) return F::template narrow<E, 1, 4, 32, 2>(a, sh, s);
-  if (sh.g == 32) return F::template narrow<E, 1, 8, 32, 1>(a, sh, s);
-  if (sh.nv == 4) return F::template wide<E, 1, 4>(a, sh, s);
-  if (sh.nv == 8) return F::template wide<E, 1, 8>(a, sh, s);
-  return F::template wide<E, 1, 32>(a, sh, s);
+template <typename F, typename E, int VEC>
+cudaError_t dispatch_small(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+  constexpr int RU = VEC == 1 ? 2 : 1;
+  if (sh.g == 32 && sh.nv == 1) return F::template narrow<E, VEC, 1, 32, 2>(a, sh, s);
+  if (sh.g == 32 && sh.nv == 2) return F::template narrow<E, VEC, 2, 32, 2>(a, sh, s);
+  if (sh.g == 32 && sh.nv == 4) return F::template narrow<E, VEC, 4, 32, RU>(a, sh, s);
+  if (sh.g == 32 && sh.nv == 8) return F::template narrow<E, VEC, 8, 32, 1>(a, sh, s);
+  if constexpr (VEC == 1) {
+    if (sh.g == 32) return F::template narrow<E, 1, 16, 32, 1>(a, sh, s);
+  }
+  if constexpr (!F::kBwd || VEC == 1) {
+    if (sh.nv == 4) return F::template wide<E, VEC, 4>(a, sh, s);
+  }
+  if (sh.nv == 8) return F::template wide<E, VEC, 8>(a, sh, s);
+  return F::template wide<E, VEC, VEC == 1 ? 32 : 16>(a, sh, s);
 }
 template <typename F>
 cudaError_t dispatch(const NormArgs& a, cudaStream_t s) {
@@ -949,7 +983,9 @@ cudaError_t dispatch(const NormArgs& a, cudaStream_t s) {
   count_launches(1);
   if (sh.vec == 8) return dispatch_vec<F, bf16, 8>(a, sh, s);
   if (sh.vec == 4) return dispatch_vec<F, float, 4>(a, sh, s);
-  return a.bf16 ? dispatch_scalar<F, bf16>(a, sh, s) : dispatch_scalar<F, float>(a, sh, s);
+  if (sh.vec == 2)
+    return a.bf16 ? dispatch_small<F, bf16, 2>(a, sh, s) : dispatch_small<F, float, 2>(a, sh, s);
+  return a.bf16 ? dispatch_small<F, bf16, 1>(a, sh, s) : dispatch_small<F, float, 1>(a, sh, s);
 }
 
 }  // namespace

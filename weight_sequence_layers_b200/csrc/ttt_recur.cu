@@ -242,7 +242,8 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
     }
     if (w == 0 && lane < cl) st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), lane), rs, bar);
     // a wait that runs out is recorded, and the rounds go on without waiting
-    mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
+    if (!mbar_try_wait_cluster(full, round >> 1 & 1))
+      mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
     __syncwarp();
     const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][s]);
     float ca[VC], cu[VC];

@@ -14,7 +14,7 @@
 //         that the epilogue of one tile runs under the products of the next. Bound by the tensor
 //         cores.
 //   split: 128 x NT tiles with the roles of rows and columns exchanged (the weights' rows are the
-//         MMA's 128 rows, NT = 16..128 tokens its columns), one tile a CTA and several CTAs an
+//         MMA's 128 rows, NT = 16, 32 or 64 tokens its columns), one tile a CTA and several CTAs an
 //         SM; the CTAs of a cluster share the contraction of one tile and add their parts through
 //         distributed shared memory in a fixed order. For few tiles: decode steps, which read the
 //         weights once (bound by HBM), and small matrices.
@@ -463,7 +463,7 @@ struct SplitArgs {
 template <int NT>
 struct SplitLayout {
   static constexpr uint32_t kA = 128 * BK * 2, kB = NT * BK * 2, kStage = kA + kB;
-  static constexpr int kStages = NT == 16 ? 3 : NT <= 64 ? 4 : 3;  // two CTAs an SM, three with NT = 16
+  static constexpr int kStages = NT == 16 ? 3 : 4;  // two CTAs an SM, three with NT = 16
   // The parts of a tile that come from the cluster's CTAs: in their own place where that is
   // small, else over the stages, once all CTAs have read these.
   static constexpr bool kOwnParts = NT <= 32;
@@ -472,7 +472,7 @@ struct SplitLayout {
   static_assert(kOwnParts || kStages * kStage >= kParts, "room for the parts");
 };
 struct __align__(8) SplitBars {
-  uint64_t full[4], empty[4], acc;
+  uint64_t full[4], empty[4], acc, parts;
   uint32_t tmem_base;
   int abort_flag;
   float join[kSumParts * 32];
@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(kSplitThreads)
       mbar_init(SB(empty[s]), 1);
     }
     mbar_init(SB(acc), 1);
+    mbar_init(SB(parts), 1);
     bars->abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(ta);
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   // (a CTA's shared memory may be written by the others once all have started)
   __syncwarp();
-  if (S > 1 && L::kOwnParts) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (S > 1 && L::kOwnParts) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -572,30 +573,32 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
   }
   __syncwarp();
-  // The outputs of this CTA: its share of the tile's tokens, 8 features (16 bytes) at a time, a
-  // token's 16 pieces side by side. The first items' operands are loaded before the sums are
-  // there.
-  const Epi& e = p.e;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (a.sums.part && warp >= 2)
     column_sums<4>(a.sums, threadIdx.x - 64, blockIdx.x, gridDim.x, bars->join);
   __syncwarp();
-  const int share = NT / S, first = t0 + rank * share, items = share * 16;
+  // The outputs of this CTA: of the tile's tokens t those with t % S = rank, 8 features (16 bytes)
+  // at a time, a token's 16 pieces side by side. Operands are loaded a batch of items ahead.
+  const Epi& e = p.e;
+  const int split_log = __ffs(S) - 1, items = (NT >> split_log) * 16;  // S is a power of two
   constexpr int kBatch = 4;
-  uint4 mu[kBatch], re[kBatch];
+  struct Operands {
+    uint4 mu[kBatch], re[kBatch];
+  } now, next;
   const int f = f0 + 8 * (threadIdx.x % 16);  // the same piece for all of a thread's items
-  auto fetch = [&](int it0) {
+  auto token_of = [&](int it) { return t0 + ((it / 16) << split_log) + rank; };
+  auto fetch = [&](int it0, Operands& o) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int it = it0 + u * kSplitThreads, t = first + it / 16;
+      const int it = it0 + u * kSplitThreads, t = token_of(it);
       if (it < items && t < p.toks && f < p.feats) {
-        const size_t o = (size_t)t * e.ld + f;
-        if (e.mul) mu[u] = *reinterpret_cast<const uint4*>(e.mul + o);
-        if (e.residual) re[u] = *reinterpret_cast<const uint4*>(e.residual + o);
+        const size_t at = (size_t)t * e.ld + f;
+        if (e.mul) o.mu[u] = *reinterpret_cast<const uint4*>(e.mul + at);
+        if (e.residual) o.re[u] = *reinterpret_cast<const uint4*>(e.residual + at);
       }
     }
   };
-  fetch(threadIdx.x);
+  fetch(threadIdx.x, now);
   float b[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) b[k] = 0.f;
@@ -612,52 +615,84 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (S > 1 && L::kOwnParts) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   else if (S > 1) cluster_sync_all();  // the MMAs of all CTAs have read their stages
   else if (!L::kOwnParts) __syncthreads();
-  // part of CTA c, token j of a CTA's share, feature i: parts[(c share + j) 128 + i]
-  if (warp >= 2) {
-    const int q = warp & 3, share_log = __ffs(share) - 1;  // the split is a power of two
-    const uint32_t part0 = stage0 + L::kOffParts + (uint32_t)(rank * share * 128 + q * 32 + lane) * 4;
+  // part of CTA c, token number j of a CTA's, feature i: parts[(c NT / S + j) 128 + i]
+  const int q = warp & 3;
+  const uint32_t part0 = stage0 + L::kOffParts + (uint32_t)((rank * NT >> split_log) * 128 + q * 32 + lane) * 4;
+  if (S == 1) {
+    if (warp >= 2)
 #pragma unroll 1
-    for (int c = 0; c < NT / 16; ++c) {
-      if (t0 + c * 16 >= p.toks) break;
-      float v[16];
-      tmem_ld16(tmem_addr(tmem, q * 32, c * 16), v);
-      tmem_wait_ld();
+      for (int c = 0; c < NT / 16 && t0 + c * 16 < p.toks; ++c) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(tmem_addr(tmem, q * 32, c * 16), v);
+        tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int t = c * 16 + j, to = t >> share_log, jj = t & (share - 1);
-        const uint32_t local = part0 + (uint32_t)jj * 512;
-        if (t0 + t < p.toks) {
-          if (S > 1)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(local, to)), "f"(v[j]) : "memory");
-          else
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(local), "f"(v[j]) : "memory");
+        for (int j = 0; j < 16; ++j)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(part0 + (c * 16 + j) * 512), "f"(v[j]) : "memory");
+      }
+    __syncthreads();
+  } else {
+    // With a place of their own the parts are counted where they arrive; over the stages a
+    // barrier of the cluster follows them.
+    const uint32_t bar = SB(parts);
+    const int valid = min(NT, p.toks - t0);
+    const int mine = valid > rank ? ((valid - rank - 1) >> split_log) + 1 : 0;  // tokens
+    if (L::kOwnParts && threadIdx.x == 0) mbar_arrive_expect_tx(bar, mine * S * 512);
+    if (warp >= 2) {
+      uint32_t to[8], bars_at[8];  // CTA j % S
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        to[k] = peer_addr(part0, k & (S - 1));
+        bars_at[k] = peer_addr(bar, k & (S - 1));
+      }
+#pragma unroll 1
+      for (int c = 0; c < NT / 16 && c * 16 < valid; ++c) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(tmem_addr(tmem, q * 32, c * 16), v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int t = c * 16 + j;
+          const uint32_t at = to[j & 7] + (t >> split_log) * 512;
+          if (t < valid) {
+            if (L::kOwnParts)
+              asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];"
+                           ::"r"(at), "f"(v[j]), "r"(bars_at[j & 7]) : "memory");
+            else
+              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[j]) : "memory");
+          }
         }
       }
+    }
+    __syncwarp();
+    if (L::kOwnParts) {
+      if (!mbar_try_wait_cluster(bar, 0)) mbar_wait_cluster(bar, 0, ab);
       __syncwarp();
+    } else {
+      cluster_sync_all();
     }
   }
-  __syncwarp();
-  if (S > 1) cluster_sync_all();
-  else __syncthreads();
   const float* parts = reinterpret_cast<const float*>(smem + L::kOffParts) + 8 * (threadIdx.x % 16);
+#pragma unroll 1
   for (int it0 = threadIdx.x; it0 < items; it0 += kBatch * kSplitThreads) {
-    if (it0 != threadIdx.x) fetch(it0);
+    fetch(it0 + kBatch * kSplitThreads, next);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int it = it0 + u * kSplitThreads, j = it / 16, t = first + j;
+      const int it = it0 + u * kSplitThreads, t = token_of(it);
       if (it >= items || t >= p.toks || f >= p.feats) continue;
       float y[8], w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) y[k] = 0.f;
       for (int c = 0; c < S; ++c) {
-        const float4* x = reinterpret_cast<const float4*>(parts + (c * share + j) * 128);
+        const float4* x = reinterpret_cast<const float4*>(parts + ((c * NT >> split_log) + it / 16) * 128);
         const float4 lo = x[0], hi = x[1];
         y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
         y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
       }
-      const size_t o = (size_t)t * e.ld + f;
-      finish8<true>(e, o, b, mu[u], re[u], y, w);
+      finish8<true>(e, (size_t)t * e.ld + f, b, now.mu[u], now.re[u], y, w);
     }
+    now = next;
   }
   tc_fence_before();
   __syncthreads();
@@ -828,21 +863,22 @@ cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bo
 
 // The kernel of a product and the CTAs that share a tile's contraction (0: the pair kernel). The
 // choice hangs on the product alone, so that its sums come out the same in any call.
-// Few rows, or few tiles that are deep: the contraction is split (200 x 2560 x 2560: 22.5 us
-// against 26.7; 1537 x 1000 x 520, a shallow one: 22.5 against the pair kernel's 18.4). The
-// backward's shallow products of few rows stay with the pair kernel too: its two then go in one
-// launch.
+// Split tiles as long as all of them are resident at a time, two an SM (543 x 3936 x 1696, 279
+// tiles: 23.4 us against the pair kernel's 25.5; 512 x 1024 x 1024: 15.4 against 20.5; beyond,
+// 200 rows' dW of 2560 x 2560: 27.6 against 21.3). With 32 rows or fewer always: the product is a
+// read of the weights. The backward's shallow products stay with the pair kernel, which takes two
+// in one launch (32 x 688 x 16: 14.3 us against 23.6).
 int tokens_of(const Product& g) {  // columns of a split tile
-  return !g.a_mn && g.rows <= 16 ? 16 : !g.a_mn && g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128;
+  return !g.a_mn && g.rows <= 16 ? 16 : !g.a_mn && g.rows <= 32 ? 32 : 64;
 }
 int split_of(const Product& g) {
-  const long long pairs = (long long)ceil_div(g.rows, PT) * ceil_div(g.cols, PT);
   const int nt = tokens_of(g), nkb = ceil_div(g.k, BK);
   const long long tiles = (long long)ceil_div(g.rows, nt) * ceil_div(g.cols, 128);
-  if ((g.rows > 64 || g.b_mn) && (pairs > kSMs / 8 || g.k < 24 * BK)) return 0;
-  // As many CTAs as are resident at a time, each with four blocks of k at least. Wide tiles stop
-  // at about one CTA per SM: their parts cost more than a second CTA brings (200 x 2560 x 2560:
-  // split 4 ways 22.5 us, 8 ways 30.8).
+  if (nt > 32 && tiles > 2 * kSMs) return 0;
+  if (g.b_mn && g.k < 24 * BK) return 0;
+  // The contraction is shared until the CTAs are as many as are resident (wide tiles: about one
+  // an SM, since their parts cost more: 200 x 2560 x 2560 19.5 us split 2 ways, 23.5 split 4
+  // ways), each with four blocks of k at least.
   const long long most = nt <= 32 ? 2 * kSMs + 29 : kSMs + 29;
   int split = 1;
   while (split < kMaxSplit && 2 * tiles * split <= most && nkb / (2 * split) >= 4) split *= 2;
@@ -877,8 +913,7 @@ cudaError_t run_split(const Product* g, int n, int split, const Sums& sums, bool
   const int nt = n > 1 ? std::max(tokens_of(g[0]), tokens_of(g[1])) : tokens_of(g[0]);
   if (nt == 16) return run_split_nt<16>(g, n, split, sums, after, err, s);
   if (nt == 32) return run_split_nt<32>(g, n, split, sums, after, err, s);
-  if (nt == 64) return run_split_nt<64>(g, n, split, sums, after, err, s);
-  return run_split_nt<128>(g, n, split, sums, after, err, s);
+  return run_split_nt<64>(g, n, split, sums, after, err, s);
 }
 
 struct BwdPlan {

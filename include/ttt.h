@@ -334,7 +334,7 @@ ttt_status inplace_ttt_bwd(int T, int d_ff, int d_model, int C, float lr, const 
  * layer norm of [B, T, d] hidden states; H > 1 with token_major = 1 is the output norm of a TTT
  * layer: O [B, H, T, d] in, rows of all heads of a token side by side out. */
 typedef struct {
-  int B, H, T;      /* rows: B * H * T < 2^31                                            */
+  int B, H, T;      /* rows: B * H * T <= 2^31 - 2^16                                    */
   int d;            /* features of a row, 1..16384                                       */
   int dtype;        /* ttt_dtype of X, residual, S, Y, dY, dS, dX                        */
   int token_major;  /* 0: Y and dY are [B, H, T, d]; 1: [B, T, H, d]                     */

@@ -226,3 +226,48 @@ def test_two_streams_at_once():
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(g[k], want[i][k]) for k in g)
+
+
+def test_backward_captured_and_replayed():
+    # the passes of one call may overlap on the device: a replay orders them as the eager call does
+    w = weights(7)
+    xs = [randn(rng(s), B, T, D, dtype=BF) for s in (21, 22)]
+    dys = [randn(rng(s), R, D, dtype=BF) for s in (23, 24)]
+    want = [backward(x, w, d) for x, d in zip(xs, dys)]
+    sync_ok()
+    x, dy = xs[0].clone(), dys[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = backward(x, w, dy)
+    for i in (1, 0, 1, 1):
+        x.copy_(xs[i])
+        dy.copy_(dys[i])
+        graph.replay()
+        sync_ok()
+        assert all(torch.equal(out[k], want[i][k]) for k in out), i
+
+
+def test_back_to_back_backwards_share_a_workspace():
+    # calls of one stream one after the other: each waits for what the one before still writes
+    M, N, K = 1500, 520, 392
+    g = rng(31)
+    X, W = randn(g, M, K, dtype=BF), randn(g, N, K, std=K ** -0.5, dtype=BF)
+    P, mul = randn(g, M, N, dtype=BF), randn(g, M, N, dtype=BF)
+    dys = [randn(g, M, N, dtype=BF) for _ in range(6)]
+    n = ttt.ttt_linear_workspace_bytes(M, N, K, 1)
+    ws = workspace(n)
+
+    def call(dy):
+        dX, dW = torch.empty_like(X), torch.empty_like(W)
+        dm, db = torch.empty_like(mul), torch.empty(N, device="cuda")
+        ttt.ttt_linear_bwd(M, N, K, "silu", X, W, P, mul, dy, dX, dW, db, dm, ws, n)
+        return dX, dW, dm, db
+
+    want = []
+    for dy in dys:
+        want.append(call(dy))
+        torch.cuda.synchronize()
+    got = [call(dy) for dy in dys]
+    sync_ok()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))

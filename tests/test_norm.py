@@ -252,3 +252,26 @@ def test_more_than_2_31_elements():
     for i in range(0, T, 1 << 16):
         total += X[i:i + (1 << 16)].to(F64).sum(0)
     assert_within("dbias", db, total, 4096 * U32 * torch.full_like(total, 0.8 * T))
+
+
+# even widths off 16 bytes (pairs) and odd ones, narrow and wide, at the edges of a thread's share
+OFF_WIDTHS = [6, 62, 66, 126, 130, 254, 258, 263, 382, 385, 510, 513, 514, 750, 1025, 1026, 2046, 2049,
+              2050, 3094, 4094, 4097, 4098, 8190, 8193, 16382]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", OFF_WIDTHS)
+def test_widths_off_sixteen_bytes(d, dtype):
+    c = case(1, 2, 23, d, dtype, token_major=d % 4 == 2, residual=d % 2 == 0, seed=d)
+    check_forward(c)
+    check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,T,d", [(2, 3, 700, 263), (1, 1, 4100, 750), (3, 2, 900, 1030), (1, 1, 3000, 2560),
+                                     (1, 2, 2500, 1021), (2, 1, 700, 4098)])
+def test_long_runs_of_wide_rows(B, H, T, d, dtype):
+    # many rows to a CTA: the ring of row copies goes round more than once, runs cross batches
+    c = case(B, H, T, d, dtype, token_major=H > 1, residual=True, seed=d)
+    check_forward(c)
+    check_backward(c)

@@ -395,3 +395,12 @@ def test_steps_equal_the_forward(dtype, gate):
     h, e = reference(c)
     assert_within("Y", Y.transpose(0, 1), h, e)
     assert_within("state", st, h[:, -1], e[:, -1])
+
+
+@pytest.mark.parametrize("dtype,gate", KINDS)
+@pytest.mark.parametrize("B,T,D", [(1, 4001, 1), (1, 2999, 63), (5, 777, 129), (2, 2300, 70), (1, 1100, 2562),
+                                   (9, 130, 2049)])
+def test_long_sequences_of_odd_widths(B, T, D, dtype, gate):
+    # clusters along the sequence, rows that start inside a 4- or 16-byte word, a last round that
+    # some CTAs have no token of
+    check(case(B, T, D, dtype, gate, seed=T, reset=0.003))

@@ -26,8 +26,10 @@ ttt_status check_norm(const ttt_norm_config* c, NormArgs* a) {
   if (c->dtype != TTT_F32 && c->dtype != TTT_BF16) return TTT_ERR_INVALID_ARG;
   if (c->token_major != 0 && c->token_major != 1) return TTT_ERR_INVALID_ARG;
   if (!isfinite(c->eps) || c->eps <= 0.f) return TTT_ERR_INVALID_ARG;
-  // row indices are 32-bit inside the kernels; element offsets are 64-bit
-  if ((long long)c->B * c->H >= (1ll << 31) || (long long)c->B * c->H * c->T >= (1ll << 31))
+  // row indices are 32-bit inside the kernels, and walks step past the last row; element offsets
+  // are 64-bit
+  constexpr long long kMaxRows = (1ll << 31) - (1 << 16);
+  if ((long long)c->B * c->H > kMaxRows || (long long)c->B * c->H * c->T > kMaxRows)
     return TTT_ERR_INVALID_ARG;
   if ((long long)c->B * c->H * c->T * c->d > (1ll << 40)) return TTT_ERR_INVALID_ARG;
   *a = NormArgs{};

@@ -455,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     fetch(pos + k * stride, k);
     mark[k] = load_reset<R, false>(a, at.b, pos + k * stride);
   }
-  join_init(js, at.cl);
   float carry[VC];
   load_carry(a.h0, a, at, carry);
+  join_init(js, at.cl);  // (behind the loads of h0, which h_final may overwrite)
   int st = 0, ahead = kStages - 1;
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
     V av[R], u[R];
@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   store_carry(a.h_final, a, at, carry);
+  if (at.cl > 1 && js.abort_flag) __nanosleep(100000);  // let what the others send land
 }
 
 // ---------------------------------------------------------------------------------- backward
@@ -579,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     fetch(pos + k * stride, k);
     mark[k] = load_reset<R, true>(a, at.b, pos + k * stride);
   }
-  join_init(js, at.cl);
   float carry[VC];
   load_carry(a.dh_final, a, at, carry);
+  join_init(js, at.cl);  // (behind the loads of dh_final, which dh0 may overwrite)
   int st = 0, ahead = kStages - 1;
   for (unsigned round = 0; round < rounds; ++round, pos += stride) {
     V av[R], na[SIG ? R : 1];
@@ -661,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   store_carry(a.dh0, a, at, carry);
+  if (at.cl > 1 && js.abort_flag) __nanosleep(100000);
 }
 
 // -------------------------------------------------------------------------------------- step

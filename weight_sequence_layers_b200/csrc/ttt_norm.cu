@@ -1,8 +1,11 @@
 // Layer norm over rows of d features with one weight group per head, forward and backward
 // (include/ttt.h).
 //
-// Both passes are bound by HBM: a row is read once into registers, reduced twice there (the
-// mean, then the centred squares: no cancellation for rows with a large mean) and written once.
+// A row is read once into registers, reduced twice there (the mean, then the centred squares: no
+// cancellation for rows with a large mean) and written once. Bound by HBM and, close behind, by the
+// instructions issued (about 18 for 32 values): 262144 x 128 bf16 forward 26 us = 5.1 TB/s,
+// 32768 x 2560 bf16 backward with dS 113 us = 5.9 TB/s and 9 us for the weight gradients' join
+// (one CTA per row with the row read three times: 734 us and 5.8 ms).
 // A row belongs to a group of threads: 8 to 32 lanes of a warp for narrow rows (several rows
 // per CTA, sums by shuffles alone), the whole CTA for wide ones. CTA (h, s) walks a contiguous
 // run of the rows of head h, so that the head's weights stay in registers, with the next rows'

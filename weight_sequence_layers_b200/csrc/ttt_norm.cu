@@ -3,7 +3,7 @@
 //
 // A row is read once into registers, reduced twice there (the mean, then the centred squares: no
 // cancellation for rows with a large mean) and written once. Bound by HBM and, close behind, by the
-// instructions issued (about 18 for 32 values): 262144 x 128 bf16 forward 26 us = 5.1 TB/s,
+// instructions issued (16 and 22 for 32 values): 262144 x 128 bf16 forward 26 us = 5.1 TB/s,
 // 32768 x 2560 bf16 backward with dS 113 us = 5.9 TB/s and 9 us for the weight gradients' join
 // (one CTA per row with the row read three times: 734 us and 5.8 ms).
 // A row belongs to a group of threads: 8 to 32 lanes of a warp for narrow rows (several rows

@@ -57,7 +57,7 @@ constexpr int kPairStages = 6, kRing = 4;
 constexpr int kTileReaders = 2 * (1 + kEpiWarps);  // leader: MMA, peer: loads, both: epilogue
 constexpr uint32_t kHalf = 128 * BK * 2;      // 16 KB: this CTA's 128 rows of A, or of B
 constexpr uint32_t kPairStage = 2 * kHalf;
-constexpr uint32_t kTurn = 32 * 32 * 4;       // an epilogue warp's block of the accumulator
+constexpr uint32_t kTurn = 32 * 32 * 4;       // an epilogue warp's float32 block, or bf16 panel
 struct __align__(8) PairBars {
   uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2], tile_full[kRing],
       tile_empty[kRing];
@@ -164,7 +164,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 // Eight neighbouring outputs from their sums y (w: scratch).
-template <bool AUX>
 __device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)[8], const uint4& mu,
                                         const uint4& re, float (&y)[8], float (&w)[8]) {
 #pragma unroll
@@ -173,12 +172,12 @@ __device__ __forceinline__ void finish8(const Epi& e, size_t o, const float (&b)
   if (e.silu)
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] *= sigm(y[k]);
-  if (AUX && e.mul) {
+  if (e.mul) {
     unpack8(mu, w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] *= w[k];
   }
-  if (AUX && e.residual) {
+  if (e.residual) {
     unpack8(re, w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] += w[k];
@@ -194,6 +193,7 @@ template <bool AUX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap tb0,
                        const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap tb1,
+                       const __grid_constant__ CUtensorMap ty0, const __grid_constant__ CUtensorMap ty1,
                        const __grid_constant__ PairArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -324,11 +324,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    // A thread reads a row of the accumulator. Alone, an output is written as such, 64 bytes of a
-    // row a thread (16384 x 2048 x 2048: 94 us; 98 by the other way). With a multiplier or a
-    // residual (AUX), rows are read and written best by several threads: each 32 x 32 block goes
-    // through shared memory (16-byte chunks swizzled by the row) and comes back as 8 columns of 4
-    // rows a thread, a row's 4 threads side by side (100 us; 108 row by row).
+    // A thread reads a row of the accumulator. Outputs alone leave by TMA: 32 rows of 64 columns go
+    // to the warp's swizzled panel and from there in one bulk store (clipped at the edges). With a
+    // multiplier, a residual or P (AUX), rows are read and written best by several threads: each
+    // 32 x 32 block goes through shared memory (16-byte chunks swizzled by the row) and comes back
+    // as 8 columns of 4 rows a thread, a row's 4 threads side by side (16384 x 2048 x 2048 with a
+    // residual: 100 us; 108 row by row).
     const int q = warp & 3, h = (warp - 2) / 4;
     float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage + (warp - 2) * kTurn);
     const int c8 = 8 * (lane % 4), r8 = lane / 4;
@@ -347,30 +348,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!mbar_wait(PB(acc_full[acc]), aph, ab)) break;
       __syncwarp();
       tc_fence_after();
+      if constexpr (!AUX) {
+        const uint32_t panel = smem_u32(turn);
+#pragma unroll 1
+        for (int cb = 2 * h; cb < 2 * h + 2; ++cb) {
+          const int c0 = n0 + 64 * cb;
+          if (lane == 0) bulk_wait_read0();  // the last store has left the panel
+          __syncwarp();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float v[32];
+            tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + cb * 64 + half * 32), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int col = c0 + half * 32 + 8 * k;
+              float y[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) y[x] = v[8 * k + x];
+              if (e.bias && col < cols) {  // columns come in eights
+                const float4 lo = *reinterpret_cast<const float4*>(e.bias + col);
+                const float4 hi = *reinterpret_cast<const float4*>(e.bias + col + 4);
+                y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
+                y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
+              }
+              if (e.silu)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) y[x] *= sigm(y[x]);
+              const uint4 o = pack8(y);
+              st_shared_v4(panel + sw128_off(lane, half * 4 + k), o.x, o.y, o.z, o.w);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && m0 < rows && c0 < cols) {
+            tma_store_2d(t < p.tiles0 ? &ty0 : &ty1, panel, c0, m0);
+            bulk_commit();
+          }
+        }
+      } else
 #pragma unroll 1
       for (int cb = 4 * h; cb < 4 * h + 4; ++cb) {
         float v[32];
-        if constexpr (!AUX) {
-          tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + cb * 32), v);
-          tmem_wait_ld();
-          const int row = m0 + lane, c0 = n0 + 32 * cb;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int col = c0 + 8 * j;
-            if (row >= rows || col >= cols) continue;
-            float b[8], y[8], w[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) b[k] = 0.f, y[k] = v[8 * j + k];
-            if (e.bias) {
-              *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(e.bias + col);
-              *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(e.bias + col + 4);
-            }
-            const uint4 none = make_uint4(0, 0, 0, 0);
-            finish8<false>(e, (size_t)row * e.ld + col, b, none, none, y, w);
-          }
-          __syncwarp();
-          continue;
-        }
         const int col = n0 + 32 * cb + c8;
         const bool cok = col < cols;  // columns come in eights
         uint4 mu[4], re[4];
@@ -408,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 turn + r * 32 + (((c8 / 4 + k) ^ (r & 7)) << 2));
             y[4 * k] = x.x; y[4 * k + 1] = x.y; y[4 * k + 2] = x.z; y[4 * k + 3] = x.w;
           }
-          finish8<true>(e, (size_t)row * e.ld + col, b, mu[i], re[i], y, w);
+          finish8(e, (size_t)row * e.ld + col, b, mu[i], re[i], y, w);
         }
         __syncwarp();
       }
@@ -420,6 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       if (++acc == 2) { acc = 0; aph ^= 1; }
     }
+    if (!AUX && lane == 0) bulk_wait0();
   }
   __syncwarp();
   tc_fence_before();
@@ -693,7 +713,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
         y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
       }
-      finish8<true>(e, (size_t)t * e.ld + f, b, now.mu[u], now.re[u], y, w);
+      finish8(e, (size_t)t * e.ld + f, b, now.mu[u], now.re[u], y, w);
     }
     now = next;
   }
@@ -844,12 +864,13 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem
 // One or two products (n); the first should be the one with the longer contraction.
 cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bool after,
                      unsigned* err, cudaStream_t s) {
-  CUtensorMap t[4];
+  CUtensorMap t[6];
   PairArgs p{};
   for (int i = 0; i < 2; ++i) {
     const Product& q = g[i < n ? i : 0];
     if (!operand_map(&t[2 * i], q.A, q.a_mn, q.rows, q.k, 128) ||
-        !operand_map(&t[2 * i + 1], q.B, q.b_mn, q.cols, q.k, 128))
+        !operand_map(&t[2 * i + 1], q.B, q.b_mn, q.cols, q.k, 128) ||
+        !make_tmap_bf16(&t[4 + i], q.e.Y, q.cols, q.rows, q.e.ld, 64, 32))
       return cudaErrorInvalidValue;
     p.p[i] = {q.rows, q.cols, ceil_div(q.k, BK), ceil_div(q.rows, PT), ceil_div(q.cols, PT), q.a_mn, q.b_mn, q.e};
     if (i < n) p.tiles += p.p[i].tm * p.p[i].tn;
@@ -858,10 +879,10 @@ cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bo
   p.counter = n > 1 ? counter : nullptr;  // tiles of one product are alike
   p.sums = sums;
   p.err = err;
-  const bool aux = g[0].e.mul || g[0].e.residual;
+  const bool aux = g[0].e.mul || g[0].e.residual || g[0].e.P;
   return launch(aux ? linear_pair_kernel<true> : linear_pair_kernel<false>,
                 2 * std::min(p.tiles, kSMs / 2), kPairThreads, kPairSmem, 1, after, s, t[0], t[1],
-                t[2], t[3], p);
+                t[2], t[3], t[4], t[5], p);
 }
 
 // The kernel of a product and the CTAs that share a tile's contraction (0: the pair kernel). The
@@ -869,8 +890,9 @@ cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bo
 // Split tiles as long as all of them are resident at a time, two an SM (543 x 3936 x 1696, 279
 // tiles: 23.4 us against the pair kernel's 25.5; 512 x 1024 x 1024: 15.4 against 20.5; beyond,
 // 200 rows' dW of 2560 x 2560: 27.6 against 21.3). With 32 rows or fewer always: the product is a
-// read of the weights. The backward's shallow products stay with the pair kernel, which takes two
-// in one launch (32 x 688 x 16: 14.3 us against 23.6).
+// read of the weights. The backward's products stay with the pair kernel, which takes two in one
+// launch, unless they are deep (1024 x 2048 x 2048, both: 33.8 us against 44; 117 x 6440 x 24 with
+// its 101 blocks of k: 29.7 against 47.8).
 int tokens_of(const Product& g) {  // columns of a split tile
   return !g.a_mn && g.rows <= 16 ? 16 : !g.a_mn && g.rows <= 32 ? 32 : 64;
 }
@@ -878,7 +900,7 @@ int split_of(const Product& g) {
   const int nt = tokens_of(g), nkb = ceil_div(g.k, BK);
   const long long tiles = (long long)ceil_div(g.rows, nt) * ceil_div(g.cols, 128);
   if (nt > 32 && tiles > 2 * kSMs) return 0;
-  if (g.b_mn && g.k < 24 * BK) return 0;
+  if (g.b_mn && nkb < 50) return 0;
   // The contraction is shared until the CTAs are as many as are resident (wide tiles: about one
   // an SM, since their parts cost more: 200 x 2560 x 2560 19.5 us split 2 ways, 23.5 split 4
   // ways), each with four blocks of k at least.

@@ -807,8 +807,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 struct Shape {
   int vec, nv, g, threads;  // g = 0: a wide row, one CTA of `threads`
 };
-// Narrow rows take as few lanes as hold the row in at most two (small accesses: eight,
-// or sixteen single elements) each.
+// Narrow rows take as few lanes as hold the row in at most two (small accesses: eight;
+// single elements in the forward: sixteen) each.
 // Wide rows: the forward takes one access (small ones: four) per thread up to 512 threads, then more.
 // The backward takes 16 values per thread: its work around a row is the same for 8 (32768 x 2560:
 // 110 us against 143 with twice the threads and two rows per barrier).
@@ -830,8 +830,8 @@ Shape shape_of(const NormArgs& a, bool bwd) {
     if (n <= 64) { s.g = 32; s.nv = 2; return s; }
     if (n <= 128) { s.g = 32; s.nv = 4; return s; }
     if (n <= 256) { s.g = 32; s.nv = 8; return s; }
-    if (n <= 512 && s.vec == 1) { s.g = 32; s.nv = 16; return s; }
-    s.nv = n <= 2048 ? 4 : n <= 4096 ? 8 : s.vec == 2 ? 16 : 32;
+    if (n <= 512 && s.vec == 1 && !bwd) { s.g = 32; s.nv = 16; return s; }
+    s.nv = n <= 2048 ? 4 : n <= 4096 ? 8 : n <= 8192 ? 16 : 32;
     if (bwd && s.vec == 2) s.nv = std::max(s.nv, 8);
   }
   s.g = 0;
@@ -971,14 +971,17 @@ cudaError_t dispatch_small(const NormArgs& a, const Shape& sh, cudaStream_t s) {
   if (sh.g == 32 && sh.nv == 2) return F::template narrow<E, VEC, 2, 32, 2>(a, sh, s);
   if (sh.g == 32 && sh.nv == 4) return F::template narrow<E, VEC, 4, 32, RU>(a, sh, s);
   if (sh.g == 32 && sh.nv == 8) return F::template narrow<E, VEC, 8, 32, 1>(a, sh, s);
-  if constexpr (VEC == 1) {
+  if constexpr (VEC == 1 && !F::kBwd) {
     if (sh.g == 32) return F::template narrow<E, 1, 16, 32, 1>(a, sh, s);
   }
   if constexpr (!F::kBwd || VEC == 1) {
     if (sh.nv == 4) return F::template wide<E, VEC, 4>(a, sh, s);
   }
   if (sh.nv == 8) return F::template wide<E, VEC, 8>(a, sh, s);
-  return F::template wide<E, VEC, VEC == 1 ? 32 : 16>(a, sh, s);
+  if constexpr (VEC == 1) {
+    if (sh.nv == 32) return F::template wide<E, VEC, 32>(a, sh, s);
+  }
+  return F::template wide<E, VEC, 16>(a, sh, s);
 }
 template <typename F>
 cudaError_t dispatch(const NormArgs& a, cudaStream_t s) {

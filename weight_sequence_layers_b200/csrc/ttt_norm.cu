@@ -493,12 +493,15 @@ __device__ __forceinline__ void slot_read(const Frag<E, VEC, NV>& f, const uint8
                                           const RowView& rv, const E* row,
                                           float2 (&v)[Frag<E, VEC, NV>::NP]) {
   Pack<E, VEC> p[NV];
+  using R = decltype(p[0].r);
+  const E* sp = reinterpret_cast<const E*>(slot + rv.off);
+  if (VEC * sizeof(E) == 16 || rv.in_slot >= f.d) {
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const E* sp = reinterpret_cast<const E*>(slot + rv.off) + f.at(n);
-    using R = decltype(p[n].r);
-    const bool held = VEC * sizeof(E) == 16 || f.at(n) < rv.in_slot;
-    p[n].r = held ? *reinterpret_cast<const R*>(sp) : *reinterpret_cast<const R*>(row + f.at(n));
+    for (int n = 0; n < NV; ++n) p[n].r = *reinterpret_cast<const R*>(sp + f.at(n));
+  } else {  // the tensor's last row, off a 16-byte boundary
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+      p[n].r = *reinterpret_cast<const R*>((f.at(n) < rv.in_slot ? sp : row) + f.at(n));
   }
   f.get(p, v);
 }

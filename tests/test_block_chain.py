@@ -271,3 +271,19 @@ def test_back_to_back_backwards_share_a_workspace():
     sync_ok()
     for a, b in zip(got, want):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_binding_refuses_what_does_not_fit():
+    cfg = ttt.make_norm_config(1, 1, 4, 64)
+    x = torch.zeros((4, 64), dtype=BF, device="cuda")
+    y = torch.empty_like(x)
+    ttt.ttt_norm_fwd(cfg, x, None, None, None, y)
+    good = (x, None, None, None, y)
+    for i, bad in ((0, x.float()), (0, x[:3]), (0, x.cpu()), (4, torch.empty((64, 4), dtype=BF, device="cuda").t()),
+                   (2, torch.ones(63, device="cuda")), (2, torch.ones(64, dtype=BF, device="cuda"))):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError, match="ttt_norm_fwd: "):
+            ttt.ttt_norm_fwd(cfg, *args)
+    ttt.ttt_norm_fwd(cfg, x.data_ptr(), None, None, None, torch.nn.Parameter(y, requires_grad=False))
+    sync_ok()

@@ -229,3 +229,16 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(ValueError, match="workspace"):
         ttt.ttt_linear_bwd(2, 8, 8, "id", 4096, 4096, None, None, 4096, dX=4096,
                            workspace=torch.zeros(4), workspace_bytes=32)
+
+
+def test_native_checks_agree_with_the_binding_s_own():
+    # what the native checks do not take, the binding's own checks name; they never take what those
+    # refuse (host tensors here: no address may come back for one)
+    from weight_sequence_layers_b200 import _bind
+    t = torch.zeros(6)
+    assert _bind.ptrs((None, 4096), (1, 1), "ff", 0) == (None, 4096)
+    for bad in ((t,), (t.view(2, 3).t(),), ("x",), (3.0,), (t.to(torch.bfloat16),), (t.to("meta"),)):
+        assert _bind.ptrs(bad, (6,), "f", 0) is None
+        assert _bind.ptrs(bad, (6,), "f", -1) is None
+    assert _bind.ptrs((t,), (6, 6), "f", 0) is None and _bind.ptrs((t,), (6,), "ff", 0) is None
+    assert _bind.ptrs([t], (6,), "f", 0) is None and _bind.ptrs((t,), (6,), "f") is None

@@ -3,7 +3,8 @@
 Argument marshalling only: every function here forwards torch tensors' device pointers,
 sizes and the current CUDA stream to the C entry point of the same name and raises
 TTTError on a non-OK status. Every step of the computation runs in the library's CUDA
-kernels; there is no fallback of any kind. Importing fails loudly if libttt.so has not
+kernels; there is no fallback of any kind. (_bind.so, where it is built, makes the argument checks
+of the block operators in one native call.) Importing fails loudly if libttt.so has not
 been built (python weight_sequence_layers_b200/build.py).
 """
 from __future__ import annotations
@@ -134,9 +135,23 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_modules = []  # torch and the native argument checks, on first use: torch loads slowly
+
+
+def _torch():
+    if not _modules:
+        import torch
+        try:
+            from . import _bind
+        except ImportError:  # not built: every check is made below, in Python
+            _bind = None
+        _modules.extend((torch, _bind))
+    return _modules[0]
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        torch = _torch()
         if torch.cuda.is_initialized():
             # current_stream() builds a Stream object: 3.4 us, a quarter of a small call
             return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
@@ -460,14 +475,20 @@ def _tensors(where, *specs):
     return out
 
 
-_TYPES = {}  # filled on first use: torch is imported by the calls that need it
+def _ptrs(where, names, tensors, counts, kinds):
+    """_tensors with the types as a string (b bfloat16, f float32, i int32, u uint8), by the native
+    checks where all is well (0.5 us for eight tensors against 4)."""
+    torch = _torch()
+    if _modules[1] is not None and torch.cuda.is_initialized():
+        p = _modules[1].ptrs(tensors, counts, kinds, torch._C._cuda_getDevice())
+        if p is not None:
+            return p
+    types = {"b": torch.bfloat16, "f": torch.float32, "i": torch.int32, "u": torch.uint8}
+    return _tensors(where, *zip(names, tensors, counts, (types[k] for k in kinds)))
 
 
-def _dtypes(code):
-    if not _TYPES:
-        import torch
-        _TYPES.update({BF16: (torch.bfloat16, torch.float32), F32: (torch.float32, torch.float32)})
-    return _TYPES[BF16 if code == BF16 else F32]
+def _kind(code):
+    return "b" if code == BF16 else "f"
 
 
 def make_norm_config(B, H, T, d, dtype="bf16", token_major=False, eps=1e-5) -> ttt_norm_config:
@@ -482,12 +503,11 @@ def ttt_norm_fwd(cfg, X, residual, weight, bias, Y, S=None, mean=None, rstd=None
     bias, S = s. X, residual, S [B,H,T,d] and Y ([B,T,H,d] if cfg.token_major) in cfg's dtype;
     weight, bias [H,d] and mean, rstd [B,H,T] float32. residual, weight, bias, S, mean and rstd
     may be None."""
-    dt, f32 = _dtypes(cfg.dtype)
-    rows, hd = cfg.B * cfg.H * cfg.T, cfg.H * cfg.d
+    k, rows, hd = _kind(cfg.dtype), cfg.B * cfg.H * cfg.T, cfg.H * cfg.d
     n = rows * cfg.d
-    p = _tensors("ttt_norm_fwd", ("X", X, n, dt), ("residual", residual, n, dt),
-                 ("weight", weight, hd, f32), ("bias", bias, hd, f32), ("Y", Y, n, dt),
-                 ("S", S, n, dt), ("mean", mean, rows, f32), ("rstd", rstd, rows, f32))
+    p = _ptrs("ttt_norm_fwd", ("X", "residual", "weight", "bias", "Y", "S", "mean", "rstd"),
+              (X, residual, weight, bias, Y, S, mean, rstd), (n, n, hd, hd, n, n, rows, rows),
+              k + k + "ff" + k + k + "ff")
     _check(_lib.ttt_norm_fwd(ctypes.byref(cfg), *p, _stream(stream)), "ttt_norm_fwd")
 
 
@@ -503,13 +523,12 @@ def ttt_norm_bwd(cfg, S, weight, mean, rstd, dY, dS, dX, dweight=None, dbias=Non
     """Layer norm backward for J = <dY, Y> + <dS, S> (dS may be None): dX (the gradient of X and
     of residual), dweight and dbias [H,d] float32 (each may be None). S is the forward's S, or
     its X without a residual. Workspace: ttt_norm_bwd_workspace_bytes(cfg)."""
-    dt, f32 = _dtypes(cfg.dtype)
-    rows, hd = cfg.B * cfg.H * cfg.T, cfg.H * cfg.d
+    k, rows, hd = _kind(cfg.dtype), cfg.B * cfg.H * cfg.T, cfg.H * cfg.d
     n = rows * cfg.d
-    p = _tensors("ttt_norm_bwd", ("S", S, n, dt), ("weight", weight, hd, f32),
-                 ("mean", mean, rows, f32), ("rstd", rstd, rows, f32), ("dY", dY, n, dt),
-                 ("dS", dS, n, dt), ("dX", dX, n, dt), ("dweight", dweight, hd, f32),
-                 ("dbias", dbias, hd, f32))
+    p = _ptrs("ttt_norm_bwd",
+              ("S", "weight", "mean", "rstd", "dY", "dS", "dX", "dweight", "dbias"),
+              (S, weight, mean, rstd, dY, dS, dX, dweight, dbias),
+              (n, hd, rows, rows, n, n, n, hd, hd), k + "fff" + k + k + k + "ff")
     _check(_lib.ttt_norm_bwd(ctypes.byref(cfg), *p, _ws(workspace, workspace_bytes),
                              int(workspace_bytes), _stream(stream)), "ttt_norm_bwd")
 
@@ -530,12 +549,10 @@ def ttt_recur_fwd(cfg, X, G, reset, h0, H, h_final=None, stream=None):
     """Gated linear recurrence h_t = a_t h_{t-1} + u_t over [B,T,D]. reset [B,T] uint8 (a nonzero
     byte starts a document: the state before that token counts as 0) and h0 [B,D] float32 may be
     None; H [B,T,D] holds every h_t, h_final [B,D] float32 (or None) the last."""
-    import torch
-    dt, f32 = _dtypes(cfg.dtype)
-    n, bd = cfg.B * cfg.T * cfg.D, cfg.B * cfg.D
-    p = _tensors("ttt_recur_fwd", ("X", X, n, dt), ("G", G, n, dt if cfg.gate else f32),
-                 ("reset", reset, cfg.B * cfg.T, torch.uint8), ("h0", h0, bd, f32),
-                 ("H", H, n, dt), ("h_final", h_final, bd, f32))
+    k, n, bd = _kind(cfg.dtype), cfg.B * cfg.T * cfg.D, cfg.B * cfg.D
+    p = _ptrs("ttt_recur_fwd", ("X", "G", "reset", "h0", "H", "h_final"),
+              (X, G, reset, h0, H, h_final), (n, n, cfg.B * cfg.T, bd, n, bd),
+              k + (k if cfg.gate else "f") + "uf" + k + "f")
     _check(_lib.ttt_recur_fwd(ctypes.byref(cfg), *p, _stream(stream)), "ttt_recur_fwd")
 
 
@@ -543,14 +560,13 @@ def ttt_recur_bwd(cfg, X, G, reset, h0, H, dH, dh_final, dX, dG, dh0=None, strea
     """Backward of ttt_recur_fwd for J = <dH, H> + <dh_final, h_final>, from the forward's inputs
     and its H: dX, dG [B,T,D] in the types of X and G, dh0 [B,D] float32. reset, h0, dh_final and
     dh0 may be None, and X with the "decay" gate."""
-    import torch
-    dt, f32 = _dtypes(cfg.dtype)
-    n, bd = cfg.B * cfg.T * cfg.D, cfg.B * cfg.D
-    gt = dt if cfg.gate else f32
-    p = _tensors("ttt_recur_bwd", ("X", X, n, dt), ("G", G, n, gt),
-                 ("reset", reset, cfg.B * cfg.T, torch.uint8), ("h0", h0, bd, f32), ("H", H, n, dt),
-                 ("dH", dH, n, dt), ("dh_final", dh_final, bd, f32), ("dX", dX, n, dt),
-                 ("dG", dG, n, gt), ("dh0", dh0, bd, f32))
+    k, n, bd = _kind(cfg.dtype), cfg.B * cfg.T * cfg.D, cfg.B * cfg.D
+    gk = k if cfg.gate else "f"
+    p = _ptrs("ttt_recur_bwd",
+              ("X", "G", "reset", "h0", "H", "dH", "dh_final", "dX", "dG", "dh0"),
+              (X, G, reset, h0, H, dH, dh_final, dX, dG, dh0),
+              (n, n, cfg.B * cfg.T, bd, n, n, bd, n, n, bd),
+              k + gk + "uf" + k + k + "f" + k + gk + "f")
     _check(_lib.ttt_recur_bwd(ctypes.byref(cfg), *p, _stream(stream)), "ttt_recur_bwd")
 
 
@@ -558,13 +574,10 @@ def ttt_recur_step(cfg, X, G, slots, state, Y, stream=None):
     """One token of cfg.B rows (cfg.T = 1) against the state cache [n_slots, D] float32, updated
     in place: row b reads and writes state[slots[b]] and Y[b] is the new state. slots [B] int32
     on the device, negative for a padding row (left untouched); None: row b has slot b."""
-    import torch
-    dt, f32 = _dtypes(cfg.dtype)
     n_slots = state.shape[0]
-    n = cfg.B * cfg.D
-    p = _tensors("ttt_recur_step", ("X", X, n, dt), ("G", G, n, dt if cfg.gate else f32),
-                 ("slots", slots, cfg.B, torch.int32), ("state", state, n_slots * cfg.D, f32),
-                 ("Y", Y, n, dt))
+    k, n = _kind(cfg.dtype), cfg.B * cfg.D
+    p = _ptrs("ttt_recur_step", ("X", "G", "slots", "state", "Y"), (X, G, slots, state, Y),
+              (n, n, cfg.B, n_slots * cfg.D, n), k + (k if cfg.gate else "f") + "if" + k)
     _check(_lib.ttt_recur_step(ctypes.byref(cfg), p[0], p[1], p[2], n_slots, p[3], p[4],
                                _stream(stream)), "ttt_recur_step")
 
@@ -582,10 +595,9 @@ def ttt_linear_fwd(M, N, K, act, X, W, bias, mul, residual, Y, P=None, workspace
     Linear's weight), mul, residual, Y and P [M,N] bf16, bias [N] float32; bias, mul, residual
     and P may be None. P receives X W^T + bias, which ttt_linear_bwd reads. N and K are multiples
     of 8. Workspace: ttt_linear_workspace_bytes(M, N, K, 0)."""
-    bf, f32 = _dtypes(BF16)
-    p = _tensors("ttt_linear_fwd", ("X", X, M * K, bf), ("W", W, N * K, bf), ("bias", bias, N, f32),
-                 ("mul", mul, M * N, bf), ("residual", residual, M * N, bf), ("Y", Y, M * N, bf),
-                 ("P", P, M * N, bf))
+    mn = M * N
+    p = _ptrs("ttt_linear_fwd", ("X", "W", "bias", "mul", "residual", "Y", "P"),
+              (X, W, bias, mul, residual, Y, P), (M * K, N * K, N, mn, mn, mn, mn), "bbfbbbb")
     _check(_lib.ttt_linear_fwd(M, N, K, ACT.get(act, act), *p, _ws(workspace, workspace_bytes),
                                int(workspace_bytes), _stream(stream)), "ttt_linear_fwd")
 
@@ -595,9 +607,9 @@ def ttt_linear_bwd(M, N, K, act, X, W, P, mul, dY, dX=None, dW=None, dbias=None,
     """Backward of ttt_linear_fwd for J = <dY, Y>: dX [M,K], dW [N,K], dmul [M,N] bf16 and dbias
     [N] float32, each written when given (the gradient of residual is dY). P is the forward's P;
     it may be None for act "id" without mul. Workspace: ttt_linear_workspace_bytes(M, N, K, 1)."""
-    bf, f32 = _dtypes(BF16)
-    p = _tensors("ttt_linear_bwd", ("X", X, M * K, bf), ("W", W, N * K, bf), ("P", P, M * N, bf),
-                 ("mul", mul, M * N, bf), ("dY", dY, M * N, bf), ("dX", dX, M * K, bf),
-                 ("dW", dW, N * K, bf), ("dbias", dbias, N, f32), ("dmul", dmul, M * N, bf))
+    mk, nk, mn = M * K, N * K, M * N
+    p = _ptrs("ttt_linear_bwd", ("X", "W", "P", "mul", "dY", "dX", "dW", "dbias", "dmul"),
+              (X, W, P, mul, dY, dX, dW, dbias, dmul), (mk, nk, mn, mn, mn, mk, nk, N, mn),
+              "bbbbbbbfb")
     _check(_lib.ttt_linear_bwd(M, N, K, ACT.get(act, act), *p, _ws(workspace, workspace_bytes),
                                int(workspace_bytes), _stream(stream)), "ttt_linear_bwd")

@@ -1,4 +1,5 @@
-"""Builds the in-tree CUDA library libttt.so for sm_100a with nvcc.
+"""Builds the in-tree CUDA library libttt.so for sm_100a with nvcc, and _bind.so, the binding's
+argument checks, with the host compiler.
 
 Each csrc/*.cu is compiled separately (in parallel) to an object, then linked into one
 shared library with the CUDA runtime linked statically, so the library loads on a host
@@ -9,15 +10,18 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libttt.so")
+BIND = os.path.join(PKG, "_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
@@ -40,7 +44,21 @@ def _compile(src: str, ptxas_v: bool) -> str:
     return obj
 
 
+def _build_bind(force: bool) -> None:
+    src = os.path.join(CSRC, "bind.cpp")
+    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= os.path.getmtime(src):
+        return
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-I", os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"], src,
+           "-o", BIND, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stderr}")
+
+
 def build(force: bool = False, ptxas_v: bool = False) -> str:
+    _build_bind(force)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     newest = max(os.path.getmtime(p) for p in _deps())
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:

@@ -866,20 +866,24 @@ cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bo
                      unsigned* err, cudaStream_t s) {
   CUtensorMap t[6];
   PairArgs p{};
-  for (int i = 0; i < 2; ++i) {
-    const Product& q = g[i < n ? i : 0];
+  const bool aux = g[0].e.mul || g[0].e.residual || g[0].e.P;
+  for (int i = 0; i < n; ++i) {
+    const Product& q = g[i];
     if (!operand_map(&t[2 * i], q.A, q.a_mn, q.rows, q.k, 128) ||
         !operand_map(&t[2 * i + 1], q.B, q.b_mn, q.cols, q.k, 128) ||
-        !make_tmap_bf16(&t[4 + i], q.e.Y, q.cols, q.rows, q.e.ld, 64, 32))
+        (!aux && !make_tmap_bf16(&t[4 + i], q.e.Y, q.cols, q.rows, q.e.ld, 64, 32)))
       return cudaErrorInvalidValue;
     p.p[i] = {q.rows, q.cols, ceil_div(q.k, BK), ceil_div(q.rows, PT), ceil_div(q.cols, PT), q.a_mn, q.b_mn, q.e};
-    if (i < n) p.tiles += p.p[i].tm * p.p[i].tn;
+    p.tiles += p.p[i].tm * p.p[i].tn;
     if (i == 0) p.tiles0 = p.tiles;
   }
+  // what the launch does not use repeats the first operand's map
+  if (n == 1) t[2] = t[3] = t[0];
+  if (aux) t[4] = t[0];
+  if (aux || n == 1) t[5] = t[0];
   p.counter = n > 1 ? counter : nullptr;  // tiles of one product are alike
   p.sums = sums;
   p.err = err;
-  const bool aux = g[0].e.mul || g[0].e.residual || g[0].e.P;
   return launch(aux ? linear_pair_kernel<true> : linear_pair_kernel<false>,
                 2 * std::min(p.tiles, kSMs / 2), kPairThreads, kPairSmem, 1, after, s, t[0], t[1],
                 t[2], t[3], t[4], t[5], p);
@@ -917,16 +921,17 @@ cudaError_t run_split_nt(const Product* g, int n, int split, const Sums& sums, b
   CUtensorMap t[4];
   SplitArgs p{};
   long long tiles = 0;
-  for (int i = 0; i < 2; ++i) {
-    const Product& q = g[i < n ? i : 0];
+  for (int i = 0; i < n; ++i) {
+    const Product& q = g[i];
     if (!operand_map(&t[2 * i], q.B, q.b_mn, q.cols, q.k, 128) ||
         !operand_map(&t[2 * i + 1], q.A, q.a_mn, q.rows, q.k, NT))
       return cudaErrorInvalidValue;
     p.p[i] = {q.cols, q.rows, ceil_div(q.k, BK), ceil_div(q.cols, 128), q.b_mn, q.a_mn, q.e};
-    if (i < n) tiles += (long long)p.p[i].tf * ceil_div(q.rows, NT);
+    tiles += (long long)p.p[i].tf * ceil_div(q.rows, NT);
     if (tiles * split >= (1ll << 31)) return cudaErrorInvalidConfiguration;
     if (i == 0) p.tiles0 = (int)tiles;
   }
+  if (n == 1) t[2] = t[3] = t[0];  // not used
   p.split = split;
   p.sums = sums;
   p.err = err;

@@ -223,3 +223,24 @@ def test_more_than_2_31_elements():
         p = c["X"].to(F64) @ c["W"].to(F64).t() + c["bias"].to(F64)
         assert_within("Y", Y[rows], act64(p, "silu"), 1e-4 * torch.ones_like(p))
         assert (want.float() - Y[rows].float()).abs().max() <= 0.05
+
+
+@pytest.mark.parametrize("act,bias,mul,residual", OPTIONS)
+@pytest.mark.parametrize("M,N,K", [(5003, 520, 136), (9000, 264, 72)])
+def test_epilogues_of_many_tiles(M, N, K, act, bias, mul, residual):
+    # enough tiles for the persistent kernel, edges inside a tile, several tiles to a CTA
+    check(case(M, N, K, act, bias, mul, residual, seed=6))
+
+
+@pytest.mark.parametrize("both", [False, True])
+def test_many_tiles_in_place(both):
+    M, N, K = 6001, 392, 136
+    c = case(M, N, K, "silu", bias=True, mul=True, residual=both, seed=4)
+    Y, _ = forward(c)
+    for which in ("mul", "residual") if both else ("mul",):
+        for _ in range(3):
+            d = dict(c, **{which: c[which].clone()})
+            ttt.ttt_linear_fwd(M, N, K, "silu", d["X"], d["W"], d["bias"], d["mul"], d["residual"],
+                               d[which])
+            sync_ok()
+            assert torch.equal(d[which], Y), which

@@ -13,8 +13,10 @@
 //   pair: 256 x 256 tiles on CTA pairs (cta_group::2), persistent, two accumulators in TMEM so
 //         that the epilogue of one tile runs under the products of the next. Bound by the tensor
 //         cores: 16384 x 2048 x 2048 backward, both products 186 us = 1.48 PFLOP/s, and by power
-//         over longer times (32768 x 9728 x 2560 with SiLU and multiplier 1.16 ms alone, 1.41 ms
-//         back to back at 1.2 GHz; a plain library product of that size 1.22 ms there).
+//         over longer times (32768 x 9728 x 2560 with SiLU and multiplier 1.14 ms alone, 1.37 ms
+//         back to back at 1.3 GHz; a plain library product of that size 1.21 ms there). Operands
+//         of the epilogue by plain loads through shared memory were 2 % slower there and 20 % on
+//         small products.
 //   split: 128 x NT tiles with the roles of rows and columns exchanged (the weights' rows are the
 //         MMA's 128 rows, NT = 16, 32 or 64 tokens its columns), one tile a CTA and several CTAs an
 //         SM; the CTAs of a cluster share the contraction of one tile and add their parts through
@@ -53,20 +55,27 @@ struct Epi {
 // ================================================================================ pair tiles
 constexpr int PT = 256;  // tile rows and columns
 constexpr int kPairThreads = 320, kEpiWarps = 8;
-constexpr int kPairStages = 6, kRing = 4;
+constexpr int kMaxStages = 6, kRing = 4;
 constexpr int kTileReaders = 2 * (1 + kEpiWarps);  // leader: MMA, peer: loads, both: epilogue
 constexpr uint32_t kHalf = 128 * BK * 2;      // 16 KB: this CTA's 128 rows of A, or of B
 constexpr uint32_t kPairStage = 2 * kHalf;
-constexpr uint32_t kTurn = 32 * 32 * 4;       // an epilogue warp's float32 block, or bf16 panel
+constexpr uint32_t kPanel = 32 * 128;         // 32 rows of 64 columns of an epilogue warp
 struct __align__(8) PairBars {
-  uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2], tile_full[kRing],
-      tile_empty[kRing];
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], tile_full[kRing],
+      tile_empty[kRing], panel_full[kEpiWarps][2];
   int ring[kRing];  // tiles handed out, a few ahead
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr size_t kPairSmem = kPairStages * kPairStage + kEpiWarps * kTurn + sizeof(PairBars) + 1024;
-static_assert(kPairSmem <= 232448, "shared memory of one CTA");
+// AUX: the epilogue has a multiplier, a residual or P, and takes two panels a warp.
+template <bool AUX>
+struct PairLayout {
+  static constexpr int kStages = AUX ? 5 : 6, kPanels = AUX ? 2 : 1;
+  static constexpr uint32_t kOffPanels = kStages * kPairStage;
+  static constexpr uint32_t kOffBars = kOffPanels + kEpiWarps * kPanels * kPanel;
+  static constexpr size_t kSmem = kOffBars + sizeof(PairBars) + 1024;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
 
 struct PairProb {
   int rows, cols, nkb;  // of D; 64-wide blocks of k
@@ -198,7 +207,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  PairBars* bars = reinterpret_cast<PairBars*>(smem + kPairStages * kPairStage + kEpiWarps * kTurn);
+  using L = PairLayout<AUX>;
+  constexpr int kPairStages = L::kStages;
+  PairBars* bars = reinterpret_cast<PairBars*>(smem + L::kOffBars);
   const uint32_t stage0 = smem_u32(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -215,6 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(PB(acc_full[a]), 1);
       mbar_init(PB(acc_empty[a]), 2 * kEpiWarps);
     }
+    for (int w = 0; w < 2 * kEpiWarps; ++w) mbar_init(PB(panel_full[w / 2][w % 2]), 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(PB(tile_full[r]), 1);
       mbar_init(PB(tile_empty[r]), kTileReaders);
@@ -324,20 +336,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    // A thread reads a row of the accumulator. Outputs alone leave by TMA: 32 rows of 64 columns go
-    // to the warp's swizzled panel and from there in one bulk store (clipped at the edges). With a
-    // multiplier, a residual or P (AUX), rows are read and written best by several threads: each
-    // 32 x 32 block goes through shared memory (16-byte chunks swizzled by the row) and comes back
-    // as 8 columns of 4 rows a thread, a row's 4 threads side by side (16384 x 2048 x 2048 with a
-    // residual: 100 us; 108 row by row).
-    const int q = warp & 3, h = (warp - 2) / 4;
-    float* turn = reinterpret_cast<float*>(smem + kPairStages * kPairStage + (warp - 2) * kTurn);
-    const int c8 = 8 * (lane % 4), r8 = lane / 4;
+    // A thread takes a row of the accumulator. Outputs leave by TMA: 32 rows of 64 columns go to a
+    // swizzled panel of the warp and from there in one bulk store (clipped at the edges). A
+    // multiplier or a residual comes into the panel the same way, ahead of the accumulator; a warp
+    // has one panel for each of its two blocks of a tile, or, with both operands, one for each of
+    // them (the maps of the second product, which a launch with operands does not have).
+    const int q = warp & 3, h = (warp - 2) / 4, ew = warp - 2;
+    const uint32_t panels = stage0 + L::kOffPanels + ew * L::kPanels * kPanel;
+    uint32_t panel_ph = 0;  // bit b: the parity of panel_full[ew][b]
     int acc = 0;
     uint32_t aph = 0;
     if (p.sums.part) {  // before the first tile's sums are there
       column_sums<kEpiWarps>(p.sums, threadIdx.x - 64, blockIdx.x, gridDim.x,
-                             reinterpret_cast<float*>(smem + kPairStages * kPairStage));
+                             reinterpret_cast<float*>(smem + L::kOffPanels));
     }
     for (int t; (t = next_tile(false)) < p.tiles;) {
       int m0, n0;
@@ -345,91 +356,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const Epi e = g.e;
       const int rows = g.rows, cols = g.cols;
       m0 += half + q * 32;
+      const bool both = AUX && e.mul && e.residual, any = AUX && (e.mul || e.residual);
+      // block b of the warp's two: its columns, whether the matrix has any of it, and its panel
+      auto col0 = [&](int b) { return n0 + 64 * (2 * h + b); };
+      auto inside = [&](int b) { return m0 < rows && col0(b) < cols; };
+      auto panel_of = [&](int b) { return panels + (L::kPanels == 2 && !both ? b : 0) * kPanel; };
+      auto fetch = [&](int b) {  // one thread
+        if (!inside(b)) return;
+        const uint32_t bar = PB(panel_full[ew][both ? 0 : b]);
+        mbar_arrive_expect_tx(bar, (both ? 2 : 1) * kPanel);
+        tma_load_2d(panel_of(b), e.mul ? &ta1 : &tb1, bar, col0(b), m0);
+        if (both) tma_load_2d(panel_of(b) + kPanel, &tb1, bar, col0(b), m0);
+      };
+      if (AUX && lane == 0) {
+        bulk_wait_read0();  // the last tile's stores have left the panels
+        if (any) fetch(0);
+        if (any && !both) fetch(1);
+      }
       if (!mbar_wait(PB(acc_full[acc]), aph, ab)) break;
       __syncwarp();
       tc_fence_after();
-      if constexpr (!AUX) {
-        const uint32_t panel = smem_u32(turn);
 #pragma unroll 1
-        for (int cb = 2 * h; cb < 2 * h + 2; ++cb) {
-          const int c0 = n0 + 64 * cb;
-          if (lane == 0) bulk_wait_read0();  // the last store has left the panel
+      for (int b = 0; b < 2; ++b) {
+        const int c0 = col0(b);
+        const uint32_t panel = panel_of(b);
+        if (lane == 0 && (!AUX || (both && b == 1))) {
+          bulk_wait_read0();  // the store before this one has left the panel
+          if (both) fetch(1);
+        }
+        __syncwarp();
+        if (any && inside(b)) {
+          const int bar = both ? 0 : b;
+          mbar_wait(PB(panel_full[ew][bar]), panel_ph >> bar & 1, ab);
+          panel_ph ^= 1u << bar;
           __syncwarp();
+        }
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float v[32];
-            tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + cb * 64 + half * 32), v);
-            tmem_wait_ld();
+        for (int part = 0; part < 2; ++part) {
+          float v[32];
+          tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + (2 * h + b) * 64 + part * 32), v);
+          tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int col = c0 + half * 32 + 8 * k;
-              float y[8];
+          for (int k = 0; k < 4; ++k) {
+            const int col = c0 + part * 32 + 8 * k;
+            const uint32_t at = panel + sw128_off(lane, part * 4 + k);
+            float y[8], w[8];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) y[x] = v[8 * k + x];
-              if (e.bias && col < cols) {  // columns come in eights
-                const float4 lo = *reinterpret_cast<const float4*>(e.bias + col);
-                const float4 hi = *reinterpret_cast<const float4*>(e.bias + col + 4);
-                y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
-                y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
-              }
-              if (e.silu)
-#pragma unroll
-                for (int x = 0; x < 8; ++x) y[x] *= sigm(y[x]);
-              const uint4 o = pack8(y);
-              st_shared_v4(panel + sw128_off(lane, half * 4 + k), o.x, o.y, o.z, o.w);
+            for (int x = 0; x < 8; ++x) y[x] = v[8 * k + x];
+            if (e.bias && col < cols) {  // columns come in eights
+              const float4 lo = *reinterpret_cast<const float4*>(e.bias + col);
+              const float4 hi = *reinterpret_cast<const float4*>(e.bias + col + 4);
+              y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
+              y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
             }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && m0 < rows && c0 < cols) {
-            tma_store_2d(t < p.tiles0 ? &ty0 : &ty1, panel, c0, m0);
-            bulk_commit();
-          }
-        }
-      } else
-#pragma unroll 1
-      for (int cb = 4 * h; cb < 4 * h + 4; ++cb) {
-        float v[32];
-        const int col = n0 + 32 * cb + c8;
-        const bool cok = col < cols;  // columns come in eights
-        uint4 mu[4], re[4];
-        float b[8];
+            if (AUX && e.P && col < cols && m0 + lane < rows)
+              *reinterpret_cast<uint4*>(e.P + (size_t)(m0 + lane) * e.ld + col) = pack8(y);
+            if (e.silu)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = m0 + 8 * i + r8;
-          const size_t o = (size_t)row * e.ld + col;
-          if (cok && row < rows) {
-            if (e.mul) mu[i] = *reinterpret_cast<const uint4*>(e.mul + o);
-            if (e.residual) re[i] = *reinterpret_cast<const uint4*>(e.residual + o);
+              for (int x = 0; x < 8; ++x) y[x] *= sigm(y[x]);
+            if (AUX && e.mul) {
+              uint4 o;
+              ld_shared_v4(at, o.x, o.y, o.z, o.w);
+              unpack8(o, w);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) y[x] *= w[x];
+            }
+            if (AUX && e.residual) {
+              uint4 o;
+              ld_shared_v4(at + (both ? kPanel : 0), o.x, o.y, o.z, o.w);
+              unpack8(o, w);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) y[x] += w[x];
+            }
+            const uint4 o = pack8(y);
+            st_shared_v4(at, o.x, o.y, o.z, o.w);
           }
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) b[k] = 0.f;
-        if (e.bias && cok) {
-          *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(e.bias + col);
-          *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(e.bias + col + 4);
-        }
-        tmem_ld32(tmem_addr(tmem, q * 32, acc * PT + cb * 32), v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<float4*>(turn + lane * 32 + ((c ^ (lane & 7)) << 2)) =
-              make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        fence_proxy_async_smem();
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + r8, row = m0 + r;
-          if (!cok || row >= rows) continue;
-          float y[8], w[8];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(
-                turn + r * 32 + (((c8 / 4 + k) ^ (r & 7)) << 2));
-            y[4 * k] = x.x; y[4 * k + 1] = x.y; y[4 * k + 2] = x.z; y[4 * k + 3] = x.w;
-          }
-          finish8(e, (size_t)row * e.ld + col, b, mu[i], re[i], y, w);
+        if (lane == 0 && inside(b)) {
+          tma_store_2d(t < p.tiles0 ? &ty0 : &ty1, panel, c0, m0);
+          bulk_commit();
         }
-        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -439,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       if (++acc == 2) { acc = 0; aph ^= 1; }
     }
-    if (!AUX && lane == 0) bulk_wait0();
+    if (lane == 0) bulk_wait0();
   }
   __syncwarp();
   tc_fence_before();
@@ -871,21 +879,27 @@ cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bo
     const Product& q = g[i];
     if (!operand_map(&t[2 * i], q.A, q.a_mn, q.rows, q.k, 128) ||
         !operand_map(&t[2 * i + 1], q.B, q.b_mn, q.cols, q.k, 128) ||
-        (!aux && !make_tmap_bf16(&t[4 + i], q.e.Y, q.cols, q.rows, q.e.ld, 64, 32)))
+        !make_tmap_bf16(&t[4 + i], q.e.Y, q.cols, q.rows, q.e.ld, 64, 32))
       return cudaErrorInvalidValue;
     p.p[i] = {q.rows, q.cols, ceil_div(q.k, BK), ceil_div(q.rows, PT), ceil_div(q.cols, PT), q.a_mn, q.b_mn, q.e};
     p.tiles += p.p[i].tm * p.p[i].tn;
     if (i == 0) p.tiles0 = p.tiles;
   }
   // what the launch does not use repeats the first operand's map
-  if (n == 1) t[2] = t[3] = t[0];
-  if (aux) t[4] = t[0];
-  if (aux || n == 1) t[5] = t[0];
+  if (n == 1) t[2] = t[3] = t[5] = t[0];
+  if (aux) {
+    if (n > 1) return cudaErrorInvalidValue;  // (the operands take the second product's maps)
+    const Epi& e = g[0].e;
+    if ((e.mul && !make_tmap_bf16(&t[2], e.mul, g[0].cols, g[0].rows, e.ld, 64, 32)) ||
+        (e.residual && !make_tmap_bf16(&t[3], e.residual, g[0].cols, g[0].rows, e.ld, 64, 32)))
+      return cudaErrorInvalidValue;
+  }
   p.counter = n > 1 ? counter : nullptr;  // tiles of one product are alike
   p.sums = sums;
   p.err = err;
   return launch(aux ? linear_pair_kernel<true> : linear_pair_kernel<false>,
-                2 * std::min(p.tiles, kSMs / 2), kPairThreads, kPairSmem, 1, after, s, t[0], t[1],
+                2 * std::min(p.tiles, kSMs / 2), kPairThreads,
+                aux ? PairLayout<true>::kSmem : PairLayout<false>::kSmem, 1, after, s, t[0], t[1],
                 t[2], t[3], t[4], t[5], p);
 }
 

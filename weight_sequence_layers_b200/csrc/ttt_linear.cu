@@ -136,13 +136,15 @@ __device__ __forceinline__ bool with_layouts(bool a_mn, bool b_mn, F f) {
   return f(Major<true>{}, Major<true>{});               // dW
 }
 // Column sums by W warps (threads 0.. of `tid`), 32 columns at a time. A column's rows fall to
-// eight parts whatever W is, so that the order of the sum is the same in every kernel.
+// eight parts whatever W is, so that the order of the sum is the same in every kernel. The walk
+// counts blocks of columns: a column's index plus a step of all CTAs can pass 2^31.
 constexpr int kSumParts = 8;
 template <int W>
 __device__ __forceinline__ void column_sums(const Sums& s, int tid, int block, int blocks, float* join) {
   const int lane = tid % 32, w = tid / 32;
-  for (int c0 = 32 * block; c0 < s.N; c0 += 32 * blocks) {
-    const int c = c0 + lane;
+  const int last = (s.N - 1) / 32;
+  for (int i = block; i <= last; i += blocks) {
+    const int c = 32 * i + lane;
 #pragma unroll
     for (int v = w; v < kSumParts; v += W) {
       float t[4] = {0.f, 0.f, 0.f, 0.f};
@@ -737,7 +739,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 
 // ============================================================================ dP, dmul, dbias
 // One pass over dY, P and mul: dP (rounded to bf16 for the products), dmul, and the column sums
-// of dP for dbias. A thread takes 8 columns of every kRowsY-th row of its CTA's rows; the CTAs'
+// of dP for dbias. A thread takes 8 columns of every kDpY-th row of its CTA's rows; the CTAs'
 // sums go to `part` [gridDim.y, N] and are added in a fixed order.
 constexpr int kDpX = 32, kDpY = 8;
 struct DpArgs {

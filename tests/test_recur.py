@@ -404,3 +404,69 @@ def test_long_sequences_of_odd_widths(B, T, D, dtype, gate):
     # clusters along the sequence, rows that start inside a 4- or 16-byte word, a last round that
     # some CTAs have no token of
     check(case(B, T, D, dtype, gate, seed=T, reset=0.003))
+
+
+# Decays above one, over stretches whose product leaves float32's range (up to 1e300) while every
+# state stays in it: zero states over a padded prefix, tiny states, growth after decay. All terms
+# are positive, so that a token's roundings stay relative to the state and K covers them as above.
+GROWTH = ["zero prefix", "tiny state", "decay then growth", "growth then decay", "huge decays"]
+
+
+def growth_case(kind, B, T, D, dtype, seed=0):
+    c = case(B, T, D, dtype, "decay", seed=seed)
+    c["X"], c["dH"] = c["X"].abs(), c["dH"].abs()
+    c["h0"] = c["dh_final"] = None
+    G = 0.5 + 0.4 * torch.rand((B, T, D), generator=rng(seed + 1), device="cuda")
+    third = max(T // 3, 1)
+    if kind in ("zero prefix", "huge decays"):
+        # features differ, and some never grow
+        big = torch.tensor([2.0, 1.1, 0.9, 1e20 if kind == "huge decays" else 8.0], device="cuda")
+        lo, hi = third, T - third
+        G[:, :lo] = big[torch.arange(D, device="cuda") % 4]
+        G[:, hi:] = big[torch.arange(D, device="cuda") % 4]
+        c["X"][:, :lo], c["X"][:, hi:] = 0, 0
+        c["dH"][:, :lo], c["dH"][:, hi:] = 0, 0
+        G[:, lo], G[:, hi] = 0.0, 0.0  # no adjoint enters the first third, no state the last
+    else:
+        n = min(T, 180)
+        up = torch.where(torch.arange(D, device="cuda") % 3 == 0, 2.0, 1.5)
+        c["X"][:, :n] = 0
+        c["dH"] *= 1e-30
+        if kind == "tiny state":       # 1e-30 grows by up to 2^150
+            G[:, :min(n, 150)] = up
+            c["h0"] = torch.full((B, D), 1e-30, device="cuda")
+        elif kind == "decay then growth":
+            G[:, :n // 2], G[:, n // 2:n] = 1 / up, up
+            c["h0"] = torch.full((B, D), 3.0, device="cuda")
+        else:
+            G[:, :n // 2], G[:, n // 2:n] = up, 1 / up
+            c["h0"] = torch.full((B, D), 3.0, device="cuda")
+    c["G"] = G
+    return c
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", GROWTH)
+@pytest.mark.parametrize("B,T,D", [(2, 100, 64), (1, 700, 65), (2, 1500, 70), (1, 2600, 33),
+                                   (40, 200, 130), (1, 900, 1021)])
+def test_decays_above_one(B, T, D, kind, dtype):
+    c = growth_case(kind, B, T, D, dtype, seed=T)
+    h, _ = reference(c)
+    assert float(h.abs().max()) < 1e38  # the states stay in range: the kernel's have to
+    check(c)
+    # a document's start inside a stretch of growth
+    c["reset"] = torch.zeros((B, T), dtype=torch.uint8, device="cuda")
+    c["reset"][:, T // 5] = 1
+    c["reset"][:, T - T // 5] = 1
+    check(c)
+
+
+def test_growth_of_one_sequence_leaves_the_others_alone():
+    # sequences (and features) are independent: one that grows changes no bit of the rest
+    c = case(3, 1300, 96, "f32", "decay", seed=2)
+    H, hf = [o.clone() for o in forward(c)]
+    c["G"][1], c["X"][1], c["h0"][1] = 2.0, 0.0, 0.0
+    H2, hf2 = forward(c)
+    for b in (0, 2):
+        assert torch.equal(H2[b], H[b]) and torch.equal(hf2[b], hf[b])
+    assert not H2[1].any() and not hf2[1].any()

@@ -22,8 +22,14 @@
 //
 // A run that holds a document's first token maps every state to its U: joins select on a flag
 // (and not by A = 0), so that an infinity or NaN of one document does not reach the next.
+//
+// Decays given as values may be above 1, and the products that join runs can then leave float32's
+// range where every state stays in it (a zero or tiny state over tokens that would double it). A
+// round in which any product of its scans is not finite is walked run after run instead, each from
+// the state that the one before left, with the arithmetic of the single-token step.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 
 #include <algorithm>
 
@@ -212,26 +218,80 @@ __device__ __forceinline__ void scan8(float (&A)[VC], float (&U)[VC], unsigned r
   }
 }
 
+// All threads of the cluster meet.
+__device__ __forceinline__ void meet(int cl) {
+  __syncwarp();
+  if (cl > 1) cluster_sync_all();
+  else __syncthreads();
+}
+// A round without products: run after run, CTA after CTA, `through` takes a run's threads from the
+// state that enters it to the one that leaves it; the state that enters the round is in CTA 0's
+// in[0], the one that leaves it comes into every CTA's A[0]. All threads of the cluster call it,
+// behind a barrier of their CTA after join_runs' last use of js.
+template <int VC, typename Through>
+__device__ __forceinline__ void join_serial(Joins<VC>& js, int cl, int rank, const Through& through) {
+  using V = Vec<VC>;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto send = [&](float* to, int cta, V h) {
+    const uint32_t at = peer_addr(smem_u32(to), cta);
+    if constexpr (VC == 1) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(h) : "memory");
+    } else {
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(at), "f"(h.x), "f"(h.y) : "memory");
+    }
+  };
+#pragma unroll 1
+  for (int r = 0; r < cl; ++r) {
+    meet(cl);  // the state that enters CTA r is in its in[0]
+    if (r != rank) continue;
+#pragma unroll 1
+    for (int q = 0; q < kWarps; ++q) {
+      if (w == q) {
+        const V h = through(*reinterpret_cast<const V*>(&js.in[q][lane * VC]));
+        if (q + 1 < kWarps) *reinterpret_cast<V*>(&js.in[q + 1][lane * VC]) = h;
+        else if (r + 1 < cl) send(&js.in[0][lane * VC], r + 1, h);
+        else if (cl == 1) *reinterpret_cast<V*>(&js.A[0][lane * VC]) = h;
+        else
+#pragma unroll 1
+          for (int c = 0; c < cl; ++c) send(&js.A[0][lane * VC], c, h);
+      }
+      __syncthreads();
+    }
+  }
+  meet(cl);
+}
+__device__ __forceinline__ bool within(float x, float most) { return fabsf(x) <= most; }
+__device__ __forceinline__ bool within(float2 x, float most) { return within(x.x, most) && within(x.y, most); }
+
 // Joins the runs' maps (A, U) (reset: the run holds a document's first token) of one round:
 // carry goes from the state that enters the round to the one that leaves it (in the layout of the
 // scans); returns the state that enters this warp's run. All threads of the cluster call it the
 // same number of times. A buffer of `cta` is free again when the next round's maps arrive: a CTA
 // sends those behind a barrier that all its threads reach after reading it, and sends into the
 // buffer again only after it has them from all.
-template <int VC>
+// WIDE: products may leave the range, where a run's A is above kSafe in size (marked beside its
+// reset). A product that did stays an infinity or NaN to the end of its lane's scan. In the scan of
+// the CTAs' maps, which all CTAs make alike, it sends the whole cluster the serial way; in the scan
+// of the runs, where the CTA's own map (lane 7's) is sound, this CTA;
+constexpr float kSafe = 3.9f;  // to the power of the 64 runs of a round: below 2^127
+template <int VC, bool WIDE, typename Through>
 __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int cl, int rank,
                                              Vec<VC> A, Vec<VC> U, bool reset, float (&carry)[VC],
-                                             unsigned* err) {
+                                             unsigned* err, const Through& through) {
   using J = Joins<VC>;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = round & 1;
   const int s = lane & 7, col = w * J::kScan + (lane >> 3);
   *reinterpret_cast<Vec<VC>*>(&js.A[w][lane * VC]) = A;
   *reinterpret_cast<Vec<VC>*>(&js.U[w][lane * VC]) = U;
-  if (lane == 0) js.run_reset[w] = reset;
+  unsigned mark = reset;
+  if constexpr (WIDE) mark |= __any_sync(~0u, !within(A, kSafe)) ? 2u : 0u;
+  if (lane == 0) js.run_reset[w] = mark;
   const uint32_t full = smem_u32(&js.full[buf]);
   if (cl > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(full, cl * (J::kCols * 8 + 4));
   __syncthreads();
-  const unsigned rs = __ballot_sync(~0u, lane < kWarps && js.run_reset[s]);
+  mark = lane < kWarps ? js.run_reset[s] : 0u;
+  const unsigned rs = __ballot_sync(~0u, mark & 1);
+  unsigned wide = WIDE ? __ballot_sync(~0u, mark & 2) : 0u;
   float a[VC], u[VC], in[VC];
 #pragma unroll
   for (int k = 0; k < VC; ++k) {
@@ -240,6 +300,10 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
     in[k] = carry[k];
   }
   scan8(a, u, rs);
+  bool own = false, out = false;  // a product of the runs' scan, of the CTAs' is out of range
+  if (wide)
+#pragma unroll
+    for (int k = 0; k < VC; ++k) own = own || !within(a[k], FLT_MAX);
   if (cl > 1) {
     const uint32_t bar = peer_addr(full, s < cl ? s : 0);  // lane s of a group sends to CTA s
 #pragma unroll
@@ -247,12 +311,15 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
       const float ta = __shfl_sync(~0u, a[k], 7, 8), tu = __shfl_sync(~0u, u[k], 7, 8);
       if (s < cl) st_async(peer_addr(smem_u32(&js.cta[buf][rank][col + 4 * k]), s), ta, tu, bar);
     }
-    if (w == 0 && lane < cl) st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), lane), rs, bar);
+    if (w == 0 && lane < cl)
+      st_async(peer_addr(smem_u32(&js.cta_reset[buf][rank]), lane), rs | (wide ? 0x100u : 0u), bar);
     // a wait that runs out is recorded, and the rounds go on without waiting
     if (!mbar_try_wait_cluster(full, round >> 1 & 1))
       mbar_wait_cluster(full, round >> 1 & 1, {&js.abort_flag, err});
     __syncwarp();
-    const unsigned crs = __ballot_sync(~0u, lane < cl && js.cta_reset[buf][s]);
+    mark = lane < cl ? js.cta_reset[buf][s] : 0u;
+    const unsigned crs = __ballot_sync(~0u, mark & 0xFF);
+    if constexpr (WIDE) wide = __ballot_sync(~0u, mark & 0x100);
     float ca[VC], cu[VC];
 #pragma unroll
     for (int k = 0; k < VC; ++k) {
@@ -261,6 +328,9 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
       cu[k] = s < cl ? q.y : 0.f;
     }
     scan8(ca, cu, crs);
+    if (wide)
+#pragma unroll
+      for (int k = 0; k < VC; ++k) out = out || !within(ca[k], FLT_MAX);
 #pragma unroll
     for (int k = 0; k < VC; ++k) {
       const float h = (crs & ((2u << s) - 1)) ? cu[k] : fmaf(ca[k], carry[k], cu[k]);  // after CTA s
@@ -277,6 +347,18 @@ __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int 
     if (cl == 1) carry[k] = __shfl_sync(~0u, h, 7, 8);
   }
   __syncthreads();
+  if constexpr (WIDE) {
+    if (wide) {  // the same in all threads of the cluster
+      const bool all = cl == 1 || __syncthreads_or(out);
+      if (__syncthreads_or(own || out)) {
+        join_serial(js, all ? cl : 1, all ? rank : 0, through);
+        if (all)
+#pragma unroll
+          for (int k = 0; k < VC; ++k) carry[k] = js.A[0][col + 4 * k];
+        __syncthreads();  // A is written by the next round
+      }
+    }
+  }
   return *reinterpret_cast<const Vec<VC>*>(&js.in[w][lane * VC]);
 }
 
@@ -294,6 +376,11 @@ struct Place {
     c = c0 + (threadIdx.x & 31) * VC;
     ok = c < a.D;
     two = c + VC <= a.D;
+  }
+  // A map's A with 1 for columns that are not the thread's own: what is read for them is not data.
+  __device__ __forceinline__ Vec<VC> only_own(Vec<VC> A) const {
+    if constexpr (VC == 1) return ok ? A : 1.f;
+    else return make_float2(ok ? A.x : 1.f, two ? A.y : 1.f);
   }
 };
 template <int VC>
@@ -428,6 +515,23 @@ struct FwdTiles {
   static constexpr int kStage = X::kBytes + G::kBytes;  // of one warp
   static constexpr size_t kSmem = (size_t)kWarps * kStagesOf<ODD> * kStage;
 };
+// A run of decays given as values, token by token from its tile (which stays until the next round's
+// first copies).
+template <typename Tl, int VC>
+struct FwdRun {
+  const uint8_t* tile;
+  unsigned odd0, rs;
+  int n;
+  __device__ __forceinline__ Vec<VC> operator()(Vec<VC> h) const {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int half = (int)(odd0 + i) & 1;
+      const auto x = Tl::X::get(tile, i, half).get();
+      h = pick(rs >> i & 1, x, fma(Tl::G::get(tile + Tl::X::kBytes, i, half).get(), h, x));
+    }
+    return h;
+  }
+};
 template <typename E, typename GT, bool SIG, int VC, int R, int CB, bool ODD>
 __global__ void __launch_bounds__(kThreads, 2)
     recur_fwd_kernel(const __grid_constant__ RecurArgs a, const int cluster) {
@@ -510,7 +614,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           mU = pick(rs >> i & 1, u[i], fma(av[i], mU, u[i]));
         }
     }
-    V h = join_runs(js, round, at.cl, at.rank, mA, mU, rs != 0, carry, a.err);
+    if constexpr (!SIG) mA = at.only_own(mA);
+    V h = join_runs<VC, !SIG>(js, round, at.cl, at.rank, mA, mU, rs != 0, carry, a.err,
+                              FwdRun<Tl, VC>{tile, odd0, rs, n});
     if (!at.ok) continue;
     E* out = H + (size_t)pos * D;
     if (rs == 0 && n == R) {
@@ -544,6 +650,21 @@ struct BwdTiles {
   static constexpr int oD = G::kBytes, oH = oD + X::kBytes, oX = oH + X::kBytes;
   static constexpr int kStage = oX + (SIG ? X::kBytes : 0);  // of one warp
   static constexpr size_t kSmem = (size_t)kWarps * kStagesOf<ODD> * kStage;
+};
+template <typename Tl, int VC>
+struct BwdRun {
+  const uint8_t* tile;
+  unsigned odd0, rs;
+  int n;
+  __device__ __forceinline__ Vec<VC> operator()(Vec<VC> c) const {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int half = (int)(odd0 + i) & 1;
+      const Vec<VC> Dt = add(Tl::X::get(tile + Tl::oD, i, half).get(), c);
+      c = pick(rs >> i & 1, all<VC>(0.f), mul(Tl::G::get(tile, i, half).get(), Dt));
+    }
+    return c;
+  }
 };
 template <typename E, typename GT, bool SIG, int VC, int R, int CB, bool ODD>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -633,7 +754,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                      mul(av[i], add(Tl::X::get(tile + Tl::oD, i, (int)(odd0 + i) & 1).get(), mU)));
         }
     }
-    V c = join_runs(js, round, at.cl, at.rank, mA, mU, rs != 0, carry, a.err);
+    if constexpr (!SIG) mA = at.only_own(mA);
+    V c = join_runs<VC, !SIG>(js, round, at.cl, at.rank, mA, mU, rs != 0, carry, a.err,
+                              BwdRun<Tl, VC>{tile, odd0, rs, n});
     if (!at.ok || n == 0) continue;
     const size_t o = (size_t)(T - 1 - pos) * D;
     auto token = [&](int i, V prev, bool first) {

@@ -26,7 +26,8 @@
 // Decays given as values may be above 1, and the products that join runs can then leave float32's
 // range where every state stays in it (a zero or tiny state over tokens that would double it). A
 // round in which any product of its scans is not finite is walked run after run instead, each from
-// the state that the one before left, with the arithmetic of the single-token step.
+// the state that the one before left, with the arithmetic of the single-token step. (The way costs
+// the decay forward of 32768 x 2560 bf16 143 -> 154 us without being taken, shorter ones nothing.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>

@@ -377,7 +377,7 @@ ttt_status ttt_norm_bwd(const ttt_norm_config* cfg, const void* S, const float* 
  * a nonzero byte the state before it counts as 0, whatever it held. */
 typedef enum { TTT_GATE_DECAY = 0, TTT_GATE_SIGMOID = 1 } ttt_gate;
 typedef struct {
-  int B, T, D;      /* sequences, tokens, features; B * T < 2^31                          */
+  int B, T, D;      /* sequences, tokens, features; B * T < 2^31, D <= 2^31 - 513         */
   int dtype;        /* ttt_dtype of X, H, dH, dX (and of G, dG with TTT_GATE_SIGMOID)     */
   int gate;         /* ttt_gate                                                          */
 } ttt_recur_config;
@@ -409,7 +409,7 @@ ttt_status ttt_recur_bwd(const ttt_recur_config* cfg, const void* X, const void*
  *  its Y row and every state stay as they were. Rows that name the same slot are applied in row
  *  order, each reading what the one before it left. A slot >= n_slots is skipped like padding
  *  and recorded as TTT_ERR_RANGE in the device error word. Without slots row b has slot b
- *  (n_slots >= B). */
+ *  (n_slots >= B). With slots B <= 2^20 (else TTT_ERR_UNSUPPORTED). */
 ttt_status ttt_recur_step(const ttt_recur_config* cfg, const void* X, const void* G,
                           const int* slots, int n_slots, float* state, void* Y, void* stream);
 

@@ -134,6 +134,23 @@ def test_recur_argument_errors():
         assert bwd(c, *p) == ttt.ERR_ALIGNMENT, i
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", ["decay", "sigmoid"])
+def test_recur_widths_whose_blocks_leave_32_bits(dtype, gate):
+    # the last block of features ends past D: no index of it may pass 2^31 - 1
+    for D in (2 ** 31 - 1, 2 ** 31 - 512):
+        c = recur_cfg(B=1, T=1, D=D, dtype=dtype, gate=gate)
+        assert ttt.lib.ttt_recur_fwd(by(c), A, A, A, A, A, A, None) == ttt.ERR_INVALID_ARG
+        assert ttt.lib.ttt_recur_bwd(by(c), *[A] * 10, None) == ttt.ERR_INVALID_ARG
+        assert ttt.lib.ttt_recur_step(by(c), A, A, A, 4, A, A, None) == ttt.ERR_INVALID_ARG
+
+
+def test_recur_step_refuses_more_rows_than_it_can_match():
+    # every row is compared with all others where slots are given
+    c = recur_cfg(B=(1 << 20) + 1, T=1, D=1)
+    assert ttt.lib.ttt_recur_step(by(c), A, A, A, 9, A, A, None) == ttt.ERR_UNSUPPORTED
+
+
 def test_recur_step_argument_errors():
     c = recur_cfg(T=1, B=4)
     step = lambda c, X, G, sl, n, st, Y: ttt.lib.ttt_recur_step(by(c), X, G, sl, n, st, Y, None)

@@ -45,6 +45,8 @@ ttt_status check_recur(const ttt_recur_config* c, RecurArgs* a) {
   if (c->dtype != TTT_F32 && c->dtype != TTT_BF16) return TTT_ERR_INVALID_ARG;
   if (c->gate != TTT_GATE_DECAY && c->gate != TTT_GATE_SIGMOID) return TTT_ERR_INVALID_ARG;
   if ((long long)c->B * c->T >= (1ll << 31)) return TTT_ERR_INVALID_ARG;
+  // blocks of features reach past the last one: their indices stay below 2^31
+  if (c->D > 2147483647 - 512) return TTT_ERR_INVALID_ARG;
   if ((long long)c->B * c->T * c->D > (1ll << 40)) return TTT_ERR_INVALID_ARG;
   *a = RecurArgs{};
   a->B = c->B; a->T = c->T; a->D = c->D;
@@ -147,6 +149,8 @@ ttt_status ttt_recur_step(const ttt_recur_config* cfg, const void* X, const void
   if (st != TTT_OK) return st;
   if (cfg->T != 1 || n_slots < 1 || !X || !G || !state || !Y) return TTT_ERR_INVALID_ARG;
   if (!slots && n_slots < cfg->B) return TTT_ERR_INVALID_ARG;
+  // every row looks for its slot among all rows'
+  if (slots && cfg->B > (1 << 20)) return TTT_ERR_UNSUPPORTED;
   if (!aligned16({X, G, slots, state, Y})) return TTT_ERR_ALIGNMENT;
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;

@@ -797,17 +797,20 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // -------------------------------------------------------------------------------------- step
-// CTA (j, b): VC features a thread of row b. Rows that name one slot are one chain: the first of
-// them applies all in order, the others leave.
+// CTA (b, y, z): a block of VC features a thread of row b; a grid's y ends at 65535, so that very wide
+// rows go on in z. Rows that name one slot are one chain: the first of them applies all in order,
+// the others leave.
 constexpr int kStepThreads = 128;
 template <typename E, typename GT, bool SIG, int VC>
 __global__ void __launch_bounds__(kStepThreads) recur_step_kernel(const __grid_constant__ RecurArgs a) {
-  const int b = blockIdx.x, c = (blockIdx.y * kStepThreads + threadIdx.x) * VC;
-  const bool ok = c < a.D;
+  const int b = blockIdx.x;
+  const unsigned block = blockIdx.z * gridDim.y + blockIdx.y;
+  const unsigned c = (block * kStepThreads + threadIdx.x) * VC;  // (below 2^31 + 2^17)
+  const bool ok = c < (unsigned)a.D;
   const int slot = a.slots ? a.slots[b] : b;
   if (slot < 0) return;
   if (slot >= a.n_slots) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.err, ERR_RANGE);
+    if (block == 0 && threadIdx.x == 0) atomicOr(a.err, ERR_RANGE);
     return;
   }
   float* st = a.state + (size_t)slot * a.D + c;
@@ -934,7 +937,8 @@ cudaError_t recur_bwd(const RecurArgs& a, cudaStream_t s) { RECUR_DISPATCH(bwd);
 cudaError_t recur_step(const RecurArgs& a, cudaStream_t s) {
   const int vc = a.D % 2 == 0 ? 2 : 1;
   const int cols = kStepThreads * vc;
-  const dim3 grid(a.B, (a.D + cols - 1) / cols);
+  const int blocks = (a.D + cols - 1) / cols, z = (blocks + 65534) / 65535;
+  const dim3 grid(a.B, (blocks + z - 1) / z, z);
   count_launches(1);
   if (vc == 2) {
     if (a.bf16 && a.sigmoid) recur_step_kernel<bf16, bf16, true, 2><<<grid, kStepThreads, 0, s>>>(a);

@@ -470,3 +470,58 @@ def test_growth_of_one_sequence_leaves_the_others_alone():
     for b in (0, 2):
         assert torch.equal(H2[b], H[b]) and torch.equal(hf2[b], hf[b])
     assert not H2[1].any() and not hf2[1].any()
+
+
+def test_float32_gates_keep_float32():
+    # A token's roundings with float32 logits do not grow with the logit: the exponential 5 U32 (two
+    # float32 steps of the hardware's and a multiply-add), the sum 1, the reciprocal 2 (one step), the
+    # gate's product 1 and the recurrence 1: 10 U32 for either gate; 24 U32 for the two of them with
+    # the difference and the products of dG (the exponential enters a (1 - a) with a factor below 1).
+    # X = 1 from a zero state gives 1 - a, X = 0 from a state of 1 gives a.
+    D = 4096
+    G = torch.linspace(-86, 86, D, device="cuda")
+    G = torch.cat([G, torch.tensor([-0.0, 0.0, 1e-3, -1e-3, 30.25, -30.25, 5.5, -5.5], device="cuda")])
+    D = G.numel()
+    cfg = ttt.make_recur_config(1, 1, D, "f32", "sigmoid")
+    g = G.to(F64)
+    a, na = torch.sigmoid(g), torch.sigmoid(-g)
+    one, zero = torch.ones(D, device="cuda"), torch.zeros(D, device="cuda")
+    # (the bounds are relative; assert_within adds half a step and the smallest normal)
+    for x, h0, ref in ((one, zero, na), (zero, one, a), (one * 3, one * 5, 3 * na + 5 * a)):
+        H, st, Y = Out(1, 1, D), h0.clone().view(1, D), Out(1, D)
+        ttt.ttt_recur_fwd(cfg, x, G, None, h0, H.t)
+        ttt.ttt_recur_step(cfg, x, G, None, st, Y.t)
+        sync_ok()
+        assert_within("H", H.check().view(-1), ref, 10 * U32 * ref)
+        assert_within("Y", Y.check().view(-1), ref, 10 * U32 * ref)
+        dX, dG, dh0 = Out(1, 1, D), Out(1, 1, D), Out(1, D)
+        ttt.ttt_recur_bwd(cfg, x, G, None, h0, H.t, one, None, dX.t, dG.t, dh0.t)
+        sync_ok()
+        assert_within("dX", dX.check().view(-1), na, 10 * U32 * na)
+        assert_within("dh0", dh0.check().view(-1), a, 10 * U32 * a)
+        s = (h0 - x).to(F64) * a * na
+        assert_within("dG", dG.check().view(-1), s, 24 * U32 * s.abs())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_logits(dtype):
+    # gates that are exactly open or shut; a NaN logit reaches its own feature only
+    inf = float("inf")
+    G = torch.tensor([inf, -inf, 1e30, -1e30, 126.0, 127.0, -87.0, float("nan"), 0.0, 200.0],
+                     device="cuda").to(DT[dtype])
+    D = G.numel()
+    X, h0 = torch.full((D,), 2.0, device="cuda").to(DT[dtype]), torch.full((D,), 5.0, device="cuda")
+    want = [5, 2, 5, 2, 5, 5, 2, float("nan"), 3.5, 5]
+    cfg = ttt.make_recur_config(1, 1, D, dtype, "sigmoid")
+    H, Y, st = torch.empty_like(X), torch.empty_like(X), h0.clone().view(1, D)
+    ttt.ttt_recur_fwd(cfg, X, G, None, h0, H)
+    ttt.ttt_recur_step(cfg, X, G, None, st, Y)
+    dX, dG, dh0 = torch.empty_like(X), torch.empty_like(X), torch.empty_like(h0)
+    ttt.ttt_recur_bwd(cfg, X, G, None, h0, H, torch.ones_like(X), None, dX, dG, dh0)
+    sync_ok()
+    for got in (H, Y, st.view(-1)):
+        for g, w in zip(got.tolist(), want):
+            assert g == w or (g != g and w != w), (got.tolist(), want)
+    ok = [i for i in range(D) if i != 7]
+    assert torch.isfinite(dX[ok].float()).all() and torch.isfinite(dG[ok].float()).all()
+    assert dh0.tolist()[0] == 1.0 and abs(dh0.tolist()[1]) < 1e-37 and dX.tolist()[1] == 1.0

@@ -73,6 +73,12 @@ __device__ __forceinline__ V pick(bool c, V a, V b) {
 
 // a = sigmoid(g) = 1 / (1 + e) and 1 - a = e a with e = exp(-g): neither is a difference. Logits
 // come held at -87 (Raw::hold), where a is 2e-38 and 1 - a is 1: beyond, e would overflow.
+// E is the logits' type. bf16: the hardware's base-2 exponential of g log2(e); the rounding of that
+// product enters the exponent, so that e is off by about a step of float32 for every unit of |g|,
+// which bf16 outputs hide (half a step of theirs is 2^16 of those). float32: with x the rounded
+// product and r what it lost (by one multiply-add, and log2(e) beyond its own float32),
+// exp(-g) = 2^x 2^r = 2^x (1 + r ln 2) to 2^-33: the hardware's own two steps are left, whatever |g|
+// is. (The library's expf and a rounded reciprocal: 32768 x 2560 forward 246 us.)
 __device__ __forceinline__ float exp2_of(float x) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
@@ -83,22 +89,43 @@ __device__ __forceinline__ float recip(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-constexpr float kNegLog2e = -1.44269504f;
+constexpr double kLog2e = 1.4426950408889634;
+constexpr float kNegLog2e = (float)-kLog2e, kNegLog2eRest = (float)(-kLog2e - (double)kNegLog2e);
+constexpr float kLn2 = 0.693147181f;
+template <typename E>
 __device__ __forceinline__ void gate_of(float g, float& a, float& na) {
-  const float e = exp2_of(g * kNegLog2e);
-  a = recip(1.f + e);
-  na = e * a;
+  if constexpr (sizeof(E) == 4) {
+    const float x = g * kNegLog2e, r = fmaf(g, kNegLog2eRest, fmaf(g, kNegLog2e, -x));
+    const float p = exp2_of(x), e = fmaf(p, r * kLn2, p);
+    a = recip(1.f + e);
+    na = e * a;
+  } else {
+    const float e = exp2_of(g * kNegLog2e);
+    a = recip(1.f + e);
+    na = e * a;
+  }
 }
+template <typename E>
 __device__ __forceinline__ void gate_of(float2 g, float2& a, float2& na) {
-  const float2 x = mul2(g, both(kNegLog2e));
-  const float2 e = make_float2(exp2_of(x.x), exp2_of(x.y));
-  const float2 q = add2(e, both(1.f));
-  a = make_float2(recip(q.x), recip(q.y));
-  na = mul2(e, a);
+  if constexpr (sizeof(E) == 4) {
+    gate_of<E>(g.x, a.x, na.x);
+    gate_of<E>(g.y, a.y, na.y);
+  } else {
+    const float2 x = mul2(g, both(kNegLog2e));
+    const float2 e = make_float2(exp2_of(x.x), exp2_of(x.y));
+    const float2 q = add2(e, both(1.f));
+    a = make_float2(recip(q.x), recip(q.y));
+    na = mul2(e, a);
+  }
 }
 
-// VC neighbouring elements of a row as they lie in memory. hold: at least -87 (0xC2AE in bf16); a
-// NaN stays one.
+// VC neighbouring elements of a row as they lie in memory. hold: at least -87 (0xC2AE in bf16), and
+// in float32, where an infinity would leave the product's rest NaN, at most 126 (1 - a is 0 from 88
+// on); a NaN stays one.
+__device__ __forceinline__ float held(float g) {
+  asm("max.NaN.f32 %0, %0, 0fC2AE0000;\n\tmin.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(g));
+  return g;
+}
 template <typename E, int VC>
 struct Raw;
 template <>
@@ -129,7 +156,7 @@ struct Raw<float, 1> {
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.L1::no_allocate.f32 %0, [%1];" : "=f"(r) : "l"(p));
   }
-  __device__ __forceinline__ void hold() { asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(r)); }
+  __device__ __forceinline__ void hold() { r = held(r); }
   __device__ __forceinline__ float get() const { return r; }
   static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 };
@@ -139,10 +166,7 @@ struct Raw<float, 2> {
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.L1::no_allocate.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "l"(p));
   }
-  __device__ __forceinline__ void hold() {
-    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(r.x));
-    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(r.y));
-  }
+  __device__ __forceinline__ void hold() { r = make_float2(held(r.x), held(r.y)); }
   __device__ __forceinline__ float2 get() const { return r; }
   static __device__ __forceinline__ void store(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 };
@@ -594,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if constexpr (SIG) {
         g.hold();
         V na;
-        gate_of(g.get(), av[i], na);
+        gate_of<GT>(g.get(), av[i], na);
         u[i] = mul(na, u[i]);
       } else {
         av[i] = g.get();
@@ -734,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       Raw<GT, VC> g = Tl::G::get(tile, i, (int)(odd0 + i) & 1);
       if constexpr (SIG) {
         g.hold();
-        gate_of(g.get(), av[i], na[i]);
+        gate_of<GT>(g.get(), av[i], na[i]);
       } else {
         av[i] = g.get();
       }
@@ -825,7 +849,7 @@ __global__ void __launch_bounds__(kStepThreads) recur_step_kernel(const __grid_c
     if constexpr (SIG) rg.hold();
     Vec<VC> aa = rg.get(), u = rx.get(), na;
     if constexpr (SIG) {
-      gate_of(aa, aa, na);
+      gate_of<GT>(aa, aa, na);
       u = mul(u, na);
     }
     h = fma(aa, h, u);

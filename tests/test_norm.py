@@ -275,3 +275,47 @@ def test_long_runs_of_wide_rows(B, H, T, d, dtype):
     c = case(B, H, T, d, dtype, token_major=H > 1, residual=True, seed=d)
     check_forward(c)
     check_backward(c)
+
+
+# widths whose last access is shared with lanes past the row's end, narrow and wide, of every access
+# size, and ones that fill their threads
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [1, 5, 33, 66, 72, 128, 200, 258, 264, 513, 750, 1021, 1400, 2049, 2560, 4098])
+def test_infinities_at_a_row_s_end(d, dtype):
+    # an infinity in the last columns is an infinity in the mean (and with its opposite a NaN), as in
+    # any other column; in dY it is an infinity in the sums over the row, and dX follows the formula
+    inf = float("inf")
+    c = case(1, 1, 12, d, dtype, seed=d)
+    clean = forward(c)
+    X, dY = c["X"].clone(), c["dY"].clone()
+    bad = {1: (d - 1, inf), 3: (d - 1, -inf), 4: (max(d - 2, 0), inf), 6: (0, inf), 7: (d - 1, float("nan"))}
+    for r, (j, v) in bad.items():
+        c["X"][0, 0, r, j] = v
+    Y, _, mean, rstd = forward(c)
+    for r in range(12):
+        if r in bad:
+            v = bad[r][1]
+            got = float(mean[0, 0, r])
+            assert got == v or (v != v and got != got), (d, r, got)
+            assert torch.isnan(Y[0, 0, r].float()).all() and not torch.isfinite(rstd[0, 0, r])
+        else:
+            assert torch.equal(Y[0, 0, r], clean[0][0, 0, r])
+    c["X"] = X
+    for r, (j, v) in bad.items():
+        c["dY"][0, 0, r, j] = v
+    dX = torch.empty_like(X)
+    ttt.ttt_norm_bwd(c["cfg"], X, c["weight"], clean[2], clean[3], c["dY"], None, dX)
+    sync_ok()
+    good = torch.empty_like(X)
+    ttt.ttt_norm_bwd(c["cfg"], X, c["weight"], clean[2], clean[3], dY, None, good)
+    sync_ok()
+    xh = (X.float() - clean[2][..., None]) * clean[3][..., None]
+    g = c["dY"].float() * c["weight"][:, None]
+    want = clean[3][..., None] * (g - g.sum(-1, keepdim=True) / d - xh * ((g * xh).sum(-1, keepdim=True) / d))
+    for r in range(12):
+        if r in bad:
+            a, b = dX[0, 0, r].float(), want[0, 0, r]
+            same = torch.where(torch.isnan(b), torch.isnan(a), a == b)
+            assert bool(same.all()), (d, r, a[~same][:4], b[~same][:4])
+        else:
+            assert torch.equal(dX[0, 0, r], good[0, 0, r])

@@ -103,8 +103,9 @@ struct Pack<E, 1> {
 
 // A thread's part of a row: NV accesses of VEC elements, `step` columns apart, as pairs (VEC = 1
 // has an odd element only with NV = 1: the pair's second half). An access past the row's end
-// reads the row's last elements again (at()): its columns are told apart by mask() only, which
-// costs less than a predicate on every access and value.
+// reads the row's last elements again (at()), or zeros behind its slot of shared memory (at_slot()):
+// its columns are told apart by mask() only, which costs less than a predicate on every access and
+// value.
 template <typename E, int VEC, int NV>
 struct Frag {
   static constexpr int NP = VEC == 1 ? (NV + 1) / 2 : NV * VEC / 2;  // pairs
@@ -112,6 +113,7 @@ struct Frag {
   __device__ __forceinline__ int col(int n) const { return first + n * step; }
   __device__ __forceinline__ bool ok(int n) const { return n < NV && col(n) < d; }
   __device__ __forceinline__ int at(int n) const { return min(col(n), d - VEC); }
+  __device__ __forceinline__ int at_slot(int n, int zeros) const { return ok(n) ? col(n) : zeros; }
   // 1 for the pair's columns that are the row's, else 0
   __device__ __forceinline__ void mask(float2 (&m)[NP]) const {
 #pragma unroll
@@ -153,7 +155,37 @@ struct Frag {
       }
   }
 };
-// The masked sum, x - mean (0 past the end), and the sum of squares of that.
+// The masked sum, x - mean (0 past the end), and the sum of squares of that. The masks multiply: an
+// infinity or NaN that is read again past the end makes a NaN of the sum, which is then taken again
+// from the row's own columns alone (selected).
+template <int NP>
+__device__ __forceinline__ float selected(const float2 (&v)[NP], const float2 (&m)[NP]) {
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) t += (m[i].x != 0.f ? v[i].x : 0.f) + (m[i].y != 0.f ? v[i].y : 0.f);
+  return t;
+}
+template <int NP>
+__device__ __forceinline__ float selected(const float2 (&v)[NP], const float2 (&x)[NP],
+                                          const float2 (&m)[NP]) {
+  float2 q[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) q[i] = mul2(v[i], x[i]);
+  return selected(q, m);
+}
+template <int N>
+__device__ __forceinline__ bool any_nan(const float (&t)[N]) {
+  bool nan = false;
+#pragma unroll
+  for (int n = 0; n < N; ++n) nan = nan || t[n] != t[n];
+  return nan;
+}
+// Sums that are not NaN stay to the last bit, whatever the rows beside them hold.
+template <int N>
+__device__ __forceinline__ void replace_nan(float (&t)[N], const float (&s)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) t[n] = t[n] != t[n] ? s[n] : t[n];
+}
 template <int NP>
 __device__ __forceinline__ float total(const float2 (&v)[NP], const float2 (&m)[NP]) {
   float2 t = mul2(v[0], m[0]);
@@ -261,8 +293,8 @@ __device__ __forceinline__ void lanes_sum(float (&v)[N]) {
 // ------------------------------------------------------------------------------ narrow rows
 // G lanes per row, NV accesses of VEC elements each, RU rows per group and step: RU rows are
 // loaded ahead while RU are reduced, which keeps enough bytes in flight. RES: with a residual,
-// which doubles a row's bytes.
-template <typename E, int VEC, int NV, int G, int RU, bool RES>
+// which doubles a row's bytes. PAST: the lanes' accesses go past the row's end.
+template <typename E, int VEC, int NV, int G, int RU, bool RES, bool PAST>
 __global__ void __launch_bounds__(kNarrowThreads, narrow_ctas(NV * VEC))
     norm_fwd_narrow(const __grid_constant__ NormArgs a, const Split sp) {
   using F = Frag<E, VEC, NV>;
@@ -319,6 +351,13 @@ __global__ void __launch_bounds__(kNarrowThreads, narrow_ctas(NV * VEC))
     }
     fetch();
     lanes_sum<G>(t);
+    if (PAST && __any_sync(~0u, any_nan(t))) {
+      float s[RU];
+#pragma unroll
+      for (int u = 0; u < RU; ++u) s[u] = selected(v[u], mk);
+      lanes_sum<G>(s);
+      replace_nan(t, s);
+    }
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       mean[u] = t[u] * inv_d;
@@ -347,7 +386,7 @@ struct Partials {
   size_t ldp;
 };
 
-template <typename E, int VEC, int NV, int G, int RU>
+template <typename E, int VEC, int NV, int G, int RU, bool PAST>
 __global__ void __launch_bounds__(kNarrowThreads, narrow_ctas(NV * VEC))
     norm_bwd_narrow(const __grid_constant__ NormArgs a, const Split sp, const Partials pt) {
   using F = Frag<E, VEC, NV>;
@@ -414,6 +453,18 @@ __global__ void __launch_bounds__(kNarrowThreads, narrow_ctas(NV * VEC))
     }
     fetch();
     lanes_sum<G>(t);
+    if (PAST && __any_sync(~0u, any_nan(t))) {
+      float2 m[F::NP];
+      float r[2 * RU];
+      f.mask(m);
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        r[2 * u] = live[u] ? selected(g[u], m) : 0.f;
+        r[2 * u + 1] = live[u] ? selected(g[u], xh[u], m) : 0.f;
+      }
+      lanes_sum<G>(r);
+      replace_nan(t, r);
+    }
 #pragma unroll
     for (int u = 0; u < RU; ++u)
       if (live[u]) {
@@ -453,10 +504,12 @@ __global__ void __launch_bounds__(kNarrowThreads, narrow_ctas(NV * VEC))
 // registers. A bulk copy moves whole 16-byte blocks: where rows start off such a boundary
 // (VEC of 1 and 2) the stage holds the blocks around the row and the row starts `off` bytes in; the
 // copy never goes past the tensor's last whole block, and the elements behind it (of the last
-// row only) are read directly.
+// row only) are read directly. Behind each slot's blocks are kZeros bytes of zeros, which accesses
+// past the row's end read (wherever in its first block the row starts).
+constexpr uint32_t kZeros = 32;
 struct Ring {
   int stages;
-  uint32_t slot;  // bytes of one row's slot, a multiple of 16
+  uint32_t slot;  // bytes of one row's slot, a multiple of 16, with the zeros at its end
 };
 struct RowView {
   uint32_t off;  // bytes from the slot's start to the row
@@ -488,20 +541,32 @@ __device__ __forceinline__ void row_copy(uint32_t slot, const E* row, uint32_t b
       ::"r"(slot), "l"(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15), "r"(bytes), "r"(bar)
       : "memory");
 }
+// A thread's accesses in a slot, from the row's start. HOLD keeps them in registers, where the compiler
+// would make them again for every row (4098 x 1021 float32 backward 23.0 us against 25.0); the
+// backward of 8 and more accesses has no registers for them (45288 x 1403: 223 us against 262).
+template <bool HOLD, typename E, int VEC, int NV>
+__device__ __forceinline__ void slot_indices(const Frag<E, VEC, NV>& f, const Ring& rg, int (&idx)[NV]) {
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    idx[n] = f.at_slot(n, (rg.slot - kZeros) / (uint32_t)sizeof(E));
+    if constexpr (HOLD) asm volatile("" : "+r"(idx[n]));
+  }
+}
 template <typename E, int VEC, int NV>
 __device__ __forceinline__ void slot_read(const Frag<E, VEC, NV>& f, const uint8_t* slot,
-                                          const RowView& rv, const E* row,
+                                          const RowView& rv, const E* row, const int (&idx)[NV],
                                           float2 (&v)[Frag<E, VEC, NV>::NP]) {
   Pack<E, VEC> p[NV];
   using R = decltype(p[0].r);
   const E* sp = reinterpret_cast<const E*>(slot + rv.off);
   if (VEC * sizeof(E) == 16 || rv.in_slot >= f.d) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) p[n].r = *reinterpret_cast<const R*>(sp + f.at(n));
+    for (int n = 0; n < NV; ++n) p[n].r = *reinterpret_cast<const R*>(sp + idx[n]);
   } else {  // the tensor's last row, off a 16-byte boundary
 #pragma unroll
     for (int n = 0; n < NV; ++n)
-      p[n].r = *reinterpret_cast<const R*>((f.at(n) < rv.in_slot ? sp : row) + f.at(n));
+      p[n].r = *reinterpret_cast<const R*>(f.ok(n) && f.col(n) >= rv.in_slot ? row + f.col(n)
+                                                                             : sp + idx[n]);
   }
   f.get(p, v);
 }
@@ -549,7 +614,11 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float (*red)[16]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = N == 1 ? c : __shfl_sync(~0u, c, n * L);
 }
-__device__ __forceinline__ void ring_init(RingBars& bars, const Ring& rg) {
+__device__ __forceinline__ void ring_init(RingBars& bars, const Ring& rg, uint8_t* slots, int nslots) {
+  for (int k = threadIdx.x; k < nslots * (int)(kZeros / 4); k += blockDim.x) {
+    const int slot = k / (int)(kZeros / 4), word = k % (int)(kZeros / 4);
+    *reinterpret_cast<uint32_t*>(slots + (size_t)(slot + 1) * rg.slot - kZeros + 4 * word) = 0u;
+  }
   for (int k = threadIdx.x; k < 2 * 4 * 16; k += blockDim.x) (&bars.red[0][0][0])[k] = 0.f;
   if (threadIdx.x == 0) {
     for (int s = 0; s < rg.stages; ++s) mbar_init(smem_u32(&bars.full[s]), 1);
@@ -630,7 +699,9 @@ __global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
   E* S = static_cast<E*>(a.S);
   const Abort ab{&bars.abort_flag, a.err};
   const int nsrc = Rs ? 2 : 1;
-  ring_init(bars, rg);
+  ring_init(bars, rg, smem, rg.stages * nsrc);
+  int idx[NV];
+  slot_indices<true>(f, rg, idx);
   Loader<E, VEC> ld(a, R, smem_u32(smem), smem_u32(bars.full));
   if (tid == 0) ld.issue(rg.stages, a, R, rg, X, nullptr, Rs);
   float2 w[F::NP], bb[F::NP], mk[F::NP];
@@ -647,10 +718,10 @@ __global__ void __launch_bounds__(512, fwd_threads(NV * VEC) / 512)
     mbar_wait(smem_u32(&bars.full[st]), ph, ab);
     float2 v[F::NP];
     float t[1];
-    slot_read(f, slot, rv, X + at.x, v);
+    slot_read(f, slot, rv, X + at.x, idx, v);
     if (Rs) {
       float2 r[F::NP];
-      slot_read(f, slot + rg.slot, rv, Rs + at.x, r);
+      slot_read(f, slot + rg.slot, rv, Rs + at.x, idx, r);
 #pragma unroll
       for (int i = 0; i < F::NP; ++i) v[i] = add2(v[i], r[i]);
     }
@@ -694,7 +765,9 @@ __global__ void __launch_bounds__(MAXT, 640 / MAXT)
   E* dX = static_cast<E*>(a.dX);
   const Abort ab{&bars.abort_flag, a.err};
   const int nsrc = dS ? 3 : 2;
-  ring_init(bars, rg);
+  ring_init(bars, rg, smem, rg.stages * nsrc);
+  int idx[NV];
+  slot_indices<RU == 2>(f, rg, idx);
   Loader<E, VEC> ld(a, R, smem_u32(smem), smem_u32(bars.full));
   if (tid == 0) ld.issue(rg.stages, a, R, rg, X, dY, dS);
   float2 w[F::NP], dw[F::NP], db[F::NP];
@@ -741,8 +814,8 @@ __global__ void __launch_bounds__(MAXT, 640 / MAXT)
         // a wait that runs out is recorded; the loop goes on without waiting, so that all
         // threads keep meeting at the barriers
         mbar_wait(smem_u32(&bars.full[st]), ph, ab);
-        slot_read(f, slot[u], row_view<E, VEC>(at.x, d, ld.total), X + at.x, xh[u]);
-        slot_read(f, slot[u] + rg.slot, row_view<E, VEC>(at.y, d, ld.total), dY + at.y, g[u]);
+        slot_read(f, slot[u], row_view<E, VEC>(at.x, d, ld.total), X + at.x, idx, xh[u]);
+        slot_read(f, slot[u] + rg.slot, row_view<E, VEC>(at.y, d, ld.total), dY + at.y, idx, g[u]);
         bwd_first(nmean[u], rstd[u], w, xh[u], g[u], dw, db, t[2 * u], t[2 * u + 1]);
         if (++st == rg.stages) { st = 0; ph ^= 1; }
         at.next(a);
@@ -758,7 +831,7 @@ __global__ void __launch_bounds__(MAXT, 640 / MAXT)
         bwd_second(rstd[u], t[2 * u] * inv_d, t[2 * u + 1] * inv_d, xh[u], g[u]);
         if (dS) {
           float2 s[F::NP];
-          slot_read(f, slot[u] + 2 * rg.slot, row_view<E, VEC>(x[u], d, ld.total), dS + x[u], s);
+          slot_read(f, slot[u] + 2 * rg.slot, row_view<E, VEC>(x[u], d, ld.total), dS + x[u], idx, s);
 #pragma unroll
           for (int i = 0; i < F::NP; ++i) g[u][i] = add2(g[u][i], s[i]);
         }
@@ -878,7 +951,7 @@ Ring ring_of(const NormArgs& a, const Shape& sh, int nsrc, bool bwd) {
   const uint32_t es = a.bf16 ? 2 : 4;
   Ring r;
   // off a 16-byte boundary a row touches up to one block more on each side
-  r.slot = sh.vec * es == 16 ? a.d * es : (a.d * es + 30) / 16 * 16;
+  r.slot = (sh.vec * es == 16 ? a.d * es : (a.d * es + 30) / 16 * 16) + kZeros;
   const uint32_t room = kRingBytes / ctas_per_sm(sh, bwd) / (nsrc * r.slot);
   r.stages = (int)std::max(1u, std::min((uint32_t)kMaxStages, room));
   return r;
@@ -903,10 +976,13 @@ struct Fwd {
   static cudaError_t narrow(const NormArgs& a, const Shape& sh, cudaStream_t s) {
     const Split sp = fwd_split(a, sh);
     const unsigned grid = (unsigned)a.H * sp.S;
-    if (a.residual)
-      norm_fwd_narrow<E, VEC, NV, G, RU, true><<<grid, sh.threads, 0, s>>>(a, sp);
-    else
-      norm_fwd_narrow<E, VEC, NV, G, 2 * RU, false><<<grid, sh.threads, 0, s>>>(a, sp);
+    if (a.d == G * NV * VEC) {
+      if (a.residual) norm_fwd_narrow<E, VEC, NV, G, RU, true, false><<<grid, sh.threads, 0, s>>>(a, sp);
+      else norm_fwd_narrow<E, VEC, NV, G, 2 * RU, false, false><<<grid, sh.threads, 0, s>>>(a, sp);
+    } else {
+      if (a.residual) norm_fwd_narrow<E, VEC, NV, G, RU, true, true><<<grid, sh.threads, 0, s>>>(a, sp);
+      else norm_fwd_narrow<E, VEC, NV, G, 2 * RU, false, true><<<grid, sh.threads, 0, s>>>(a, sp);
+    }
     return cudaGetLastError();
   }
   template <typename E, int VEC, int NV>
@@ -926,8 +1002,11 @@ struct Bwd {
   template <typename E, int VEC, int NV, int G, int RU>
   static cudaError_t narrow(const NormArgs& a, const Shape& sh, cudaStream_t s) {
     const Split sp = bwd_split(a, sh);
-    norm_bwd_narrow<E, VEC, NV, G, RU>
-        <<<(unsigned)a.H * sp.S, sh.threads, 0, s>>>(a, sp, partials_of(a, sp));
+    const unsigned grid = (unsigned)a.H * sp.S;
+    if (a.d == G * NV * VEC)
+      norm_bwd_narrow<E, VEC, NV, G, RU, false><<<grid, sh.threads, 0, s>>>(a, sp, partials_of(a, sp));
+    else
+      norm_bwd_narrow<E, VEC, NV, G, RU, true><<<grid, sh.threads, 0, s>>>(a, sp, partials_of(a, sp));
     return cudaGetLastError();
   }
   template <typename E, int VEC, int NV>

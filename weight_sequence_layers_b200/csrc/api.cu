@@ -32,13 +32,17 @@ unsigned* error_word(cudaError_t* e) {
   *e = cudaGetDevice(&dev);
   if (*e != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     if (*e == cudaSuccess) *e = cudaErrorInvalidDevice;
+    (void)cudaGetLastError();  // (launch_status)
     return nullptr;
   }
   std::lock_guard<std::mutex> lk(g_err_mu);
   if (!g_err_ptr[dev]) {
     void* p = nullptr;
     *e = cudaGetSymbolAddress(&p, g_error_word);
-    if (*e != cudaSuccess) return nullptr;
+    if (*e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
     g_err_ptr[dev] = static_cast<unsigned*>(p);
   }
   return g_err_ptr[dev];
@@ -107,7 +111,6 @@ Path bwd_path(const LayerArgs& a, bool g_saved) {
   return PATH_NONE;
 }
 
-ttt_status launch_status(cudaError_t e) { return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA; }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -144,6 +147,14 @@ __global__ void selftest_wait_kernel(unsigned spin_limit, unsigned* err) {
 }
 
 }  // namespace
+
+// The runtime keeps an error until it is asked for it: one that a call has reported must not be found
+// by the next call's check of its own launch.
+ttt_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return TTT_OK;
+  (void)cudaGetLastError();
+  return TTT_ERR_CUDA;
+}
 
 unsigned* current_error_word() {
   cudaError_t e;
@@ -591,16 +602,17 @@ ttt_status inplace_ttt_bwd_docs(int T, int d_ff, int d_model, int C, float lr, c
 
 ttt_status ttt_get_device_error(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(s) != cudaSuccess) return TTT_ERR_CUDA;
-  cudaError_t e;
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return launch_status(e);
   unsigned* err = error_word(&e);
   if (!err) return TTT_ERR_CUDA;
   unsigned h = 0;
-  if (cudaMemcpy(&h, err, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return TTT_ERR_CUDA;
+  e = cudaMemcpy(&h, err, sizeof(h), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return launch_status(e);
   if (h) {
     const unsigned zero = 0;
-    if (cudaMemcpy(err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
-      return TTT_ERR_CUDA;
+    e = cudaMemcpy(err, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) return launch_status(e);
     return (h & ERR_WAIT_TIMEOUT) ? TTT_ERR_TIMEOUT : TTT_ERR_RANGE;
   }
   return TTT_OK;

@@ -9,6 +9,9 @@
 #include "../../include/ttt.h"
 #include "kernels.h"
 
+namespace tttk {
+ttt_status launch_status(cudaError_t e);  // api.cu
+}
 using namespace tttk;
 
 namespace {
@@ -18,8 +21,6 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
     if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
   return true;
 }
-
-ttt_status status_of(cudaError_t e) { return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA; }
 
 ttt_status check_norm(const ttt_norm_config* c, NormArgs* a) {
   if (!c || c->B < 1 || c->H < 1 || c->T < 1 || c->d < 1) return TTT_ERR_INVALID_ARG;
@@ -84,7 +85,7 @@ ttt_status ttt_norm_fwd(const ttt_norm_config* cfg, const void* X, const void* r
   a.mean = mean; a.rstd = rstd;
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;
-  return status_of(norm_fwd(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(norm_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ttt_norm_bwd_workspace_bytes(const ttt_norm_config* cfg) {
@@ -109,7 +110,7 @@ ttt_status ttt_norm_bwd(const ttt_norm_config* cfg, const void* S, const float* 
   a.dbias = dbias; a.ws = workspace;
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;
-  return status_of(norm_bwd(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(norm_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 ttt_status ttt_recur_fwd(const ttt_recur_config* cfg, const void* X, const void* G,
@@ -123,7 +124,7 @@ ttt_status ttt_recur_fwd(const ttt_recur_config* cfg, const void* X, const void*
   a.X = X; a.G = G; a.reset = reset; a.h0 = h0; a.H = H; a.h_final = h_final;
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;
-  return status_of(recur_fwd(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(recur_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 ttt_status ttt_recur_bwd(const ttt_recur_config* cfg, const void* X, const void* G,
@@ -139,7 +140,7 @@ ttt_status ttt_recur_bwd(const ttt_recur_config* cfg, const void* X, const void*
   a.dX = dX; a.dG = dG; a.dh0 = dh0;
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;
-  return status_of(recur_bwd(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(recur_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 ttt_status ttt_recur_step(const ttt_recur_config* cfg, const void* X, const void* G,
@@ -155,7 +156,7 @@ ttt_status ttt_recur_step(const ttt_recur_config* cfg, const void* X, const void
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;
   a.X = X; a.G = G; a.slots = slots; a.n_slots = n_slots; a.state = state; a.H = Y;
-  return status_of(recur_step(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(recur_step(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ttt_linear_workspace_bytes(int M, int N, int K, int for_bwd) {
@@ -179,7 +180,7 @@ ttt_status ttt_linear_fwd(int M, int N, int K, int act, const void* X, const voi
   a.ws = workspace;
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;
-  return status_of(linear_fwd(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(linear_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 ttt_status ttt_linear_bwd(int M, int N, int K, int act, const void* X, const void* W,
@@ -200,7 +201,7 @@ ttt_status ttt_linear_bwd(int M, int N, int K, int act, const void* X, const voi
   a.dX = dX; a.dW = dW; a.dbias = dbias; a.dmul = dmul; a.ws = workspace;
   a.err = current_error_word();
   if (!a.err) return TTT_ERR_CUDA;
-  return status_of(linear_bwd(a, static_cast<cudaStream_t>(stream)));
+  return launch_status(linear_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

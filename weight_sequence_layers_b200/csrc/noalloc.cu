@@ -12,6 +12,7 @@
 namespace tttk {
 
 ttt_status check_config(const ttt_config* c);  // api.cu
+ttt_status launch_status(cudaError_t e);
 
 namespace {
 
@@ -77,5 +78,5 @@ extern "C" ttt_status ttt_chunk_bwd_noalloc(const ttt_config* cfg, const void* Q
   a.dO = dO; a.dW_final = dW_final; a.dQ = dQ; a.dK = dK; a.dV = dV; a.dbeta = dbeta;
   a.dW0 = dW0; a.ws = scratch; a.ws_bytes = TTT_NOALLOC_SCRATCH_BYTES; a.err = err;
   a.O_in = O; a.W_final_in = W_final; a.dgamma = dgamma;
-  return tc_bwd(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  return launch_status(tc_bwd(a, static_cast<cudaStream_t>(stream)));
 }

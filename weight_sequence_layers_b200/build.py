@@ -1,5 +1,5 @@
-"""Builds the in-tree CUDA library libttt.so for sm_100a with nvcc, and _bind.so, the binding's
-argument checks, with the host compiler.
+"""Builds the in-tree CUDA library libttt.so for sm_100a with nvcc, and where torch is installed
+_bind.so, the binding's argument checks, with the host compiler.
 
 Each csrc/*.cu is compiled separately (in parallel) to an object, then linked into one
 shared library with the CUDA runtime linked statically, so the library loads on a host
@@ -44,21 +44,54 @@ def _compile(src: str, ptxas_v: bool) -> str:
     return obj
 
 
-def _build_bind(force: bool) -> None:
-    src = os.path.join(CSRC, "bind.cpp")
-    if not force and os.path.exists(BIND) and os.path.getmtime(BIND) >= os.path.getmtime(src):
-        return
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def _bind_stamp(torch_dir: str) -> str:
+    """What _bind.so was built against: it is built again where the interpreter or torch changes."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return f"{sys.version}\n{torch_dir}\n{f.read()}"
+
+
+def _build_bind(force: bool = False) -> bool:
+    """Builds _bind.so where torch and its headers are there; the binding works without it, and the
+    library needs neither. Returns whether it is built and up to date."""
+    src, stamp_file = os.path.join(CSRC, "bind.cpp"), os.path.join(OBJ, "bind.stamp")
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return False
+    torch = spec.submodule_search_locations[0]
+    try:
+        stamp = _bind_stamp(torch)
+    except OSError:
+        return False
+    old = open(stamp_file).read() if os.path.exists(stamp_file) else None
+    if not force and old == stamp and os.path.exists(BIND) and \
+            os.path.getmtime(BIND) >= os.path.getmtime(src):
+        return True
+    if os.path.exists(BIND):
+        os.remove(BIND)  # one built against another torch must not be loaded
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            "-I", os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"], src,
            "-o", BIND, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stderr if r.returncode != 0 else None
+    except OSError as e:  # no compiler
+        failed = str(e)
+    if failed is not None:
+        sys.stderr.write(f"_bind.so is not built (its checks are then made in Python): {failed}\n")
+        return False
+    os.makedirs(OBJ, exist_ok=True)
+    with open(stamp_file, "w") as f:
+        f.write(stamp)
+    return True
 
 
 def build(force: bool = False, ptxas_v: bool = False) -> str:
+    lib = _build_lib(force, ptxas_v)
     _build_bind(force)
+    return lib
+
+
+def _build_lib(force: bool, ptxas_v: bool) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     newest = max(os.path.getmtime(p) for p in _deps())
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:

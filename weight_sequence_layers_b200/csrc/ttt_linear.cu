@@ -911,8 +911,9 @@ cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bo
 // tiles: 23.4 us against the pair kernel's 25.5; 512 x 1024 x 1024: 15.4 against 20.5; beyond,
 // 200 rows' dW of 2560 x 2560: 27.6 against 21.3). With 32 rows or fewer always: the product is a
 // read of the weights. The backward's products stay with the pair kernel, which takes two in one
-// launch, unless they are deep (1024 x 2048 x 2048, both: 33.8 us against 44; 117 x 6440 x 24 with
-// its 101 blocks of k: 29.7 against 47.8).
+// launch, unless they are deep (1024 x 2048 x 2048, both: 33.8 us against 44; 1024 x 1024 x 1024,
+// 17.4 against 25.0; 117 x 6440 x 24 with its 101 blocks of k: 29.7 against 47.8). The price is a call
+// for one product of few tiles and a middling depth: dX of 64 x 2048 x 2048 takes 19.5 us, split 15.0.
 int tokens_of(const Product& g) {  // columns of a split tile
   return !g.a_mn && g.rows <= 16 ? 16 : !g.a_mn && g.rows <= 32 ? 32 : 64;
 }
@@ -921,12 +922,15 @@ int split_of(const Product& g) {
   const long long tiles = (long long)ceil_div(g.rows, nt) * ceil_div(g.cols, 128);
   if (nt > 32 && tiles > 2 * kSMs) return 0;
   if (g.b_mn && nkb < 50) return 0;
-  // The contraction is shared until the CTAs are as many as are resident (wide tiles: about one
-  // an SM, since their parts cost more: 200 x 2560 x 2560 19.5 us split 2 ways, 23.5 split 4
-  // ways), each with four blocks of k at least.
-  const long long most = nt <= 32 ? 2 * kSMs + 29 : kSMs + 29;
+  // The contraction is shared as long as all CTAs stay resident (a cluster lies within one GPC, so
+  // that fewer fit with the larger ones: kResident at two an SM, by the occupancy query; three with
+  // 16 tokens), each with four blocks of k at least. us on both sides of the limit, K = 2560, for a
+  // split of 2 / 4: 16 tokens, limit 426 CTAs: 23.3 / 22.6 at 100 tiles, 24.7 / 28.0 at 111; 32 tokens,
+  // limit 284: 20.5 / 18.7 at 70, 20.5 / 24.6 at 74; 64 tokens: 22.6 / 22.3 at 70, 23.1 / 28.8 at 74.
+  constexpr int kResident[kMaxSplit + 1] = {0, 2 * kSMs, 2 * kSMs, 0, 284, 0, 0, 0, 264};
+  auto resident = [&](int split) { return kResident[split] * (nt == 16 ? 3 : 2) / 2; };
   int split = 1;
-  while (split < kMaxSplit && 2 * tiles * split <= most && nkb / (2 * split) >= 4) split *= 2;
+  while (split < kMaxSplit && 2 * tiles * split <= resident(2 * split) && nkb / (2 * split) >= 4) split *= 2;
   return split;
 }
 

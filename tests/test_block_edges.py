@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import weight_sequence_layers_b200 as ttt
-from _block import rng, sync_ok, workspace
+from _block import F64, U32, assert_within, rng, sync_ok, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,79 @@ def test_a_refused_launch_is_not_the_next_call_s():
             except ttt.TTTError as err:
                 raise AssertionError(f"{after} after a refused {name}: {err}")
         sync_ok()
+
+
+# Past 2^31 elements, with small whole numbers in every input: sums of products of them are whole
+# and below 2^24, exact in float32 in any order, so that one row too few or twice shows.
+def ints(g, *shape, lo=-3, hi=4):
+    t = torch.empty(shape, dtype=BF, device="cuda")
+    flat = t.view(-1)
+    for i in range(0, flat.numel(), 1 << 28):
+        part = flat[i:i + (1 << 28)]
+        part.copy_(torch.randint(lo, hi, part.shape, generator=g, device="cuda", dtype=torch.int8))
+    return t
+
+
+def test_norm_weight_gradients_past_2_31_elements():
+    d, T = 4096, (1 << 19) + 3
+    g = rng(21)
+    cfg = ttt.make_norm_config(1, 1, T, d)
+    S, dY = ints(g, T, d), ints(g, T, d)
+    mean, rstd = torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")  # xh = S
+    dX, dw, db = torch.empty_like(S), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    n = ttt.ttt_norm_bwd_workspace_bytes(cfg)
+    ttt.ttt_norm_bwd(cfg, S, None, mean, rstd, dY, None, dX, dw, db, workspace(n), n)
+    sync_ok()
+    sw, sb = torch.zeros(d, dtype=F64, device="cuda"), torch.zeros(d, dtype=F64, device="cuda")
+    for i in range(0, T, 1 << 15):
+        y, s = dY[i:i + (1 << 15)].to(F64), S[i:i + (1 << 15)].to(F64)
+        sb += y.sum(0)
+        sw += (y * s).sum(0)
+    assert torch.equal(db.to(F64), sb) and torch.equal(dw.to(F64), sw)
+    for rows in (slice(0, 5), slice(T - 5, T)):
+        y, s = dY[rows].to(F64), S[rows].to(F64)
+        c1, c2 = y.mean(-1, keepdim=True), (y * s).mean(-1, keepdim=True)  # sums exact, quotients rounded
+        assert_within("dX", dX[rows], y - c1 - s * c2, 4 * U32 * (y.abs() + c1.abs() + 2 * (s * c2).abs()))
+
+
+def test_linear_backward_past_2_31_elements():
+    M, N, K = (1 << 17) + 5, 16392, 64
+    g = rng(22)
+    dY, P, mul, X, W = ints(g, M, N), ints(g, M, N), ints(g, M, N), ints(g, M, K), ints(g, N, K)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    dbias, dmul = torch.empty(N, device="cuda"), torch.empty_like(dY)
+    n = ttt.ttt_linear_workspace_bytes(M, N, K, 1)
+    ttt.ttt_linear_bwd(M, N, K, "id", X, W, P, mul, dY, dX, dW, dbias, dmul, workspace(n), n)
+    sync_ok()
+    sW, sb = torch.zeros((N, K), dtype=F64, device="cuda"), torch.zeros(N, dtype=F64, device="cuda")
+    for i in range(0, M, 1 << 13):
+        r = slice(i, i + (1 << 13))
+        assert torch.equal(dmul[r], dY[r] * P[r])  # up to 9: exact
+        dp = dY[r].to(F64) * mul[r].to(F64)
+        sb += dp.sum(0)
+        sW += dp.t() @ X[r].to(F64)
+        assert torch.equal(dX[r], (dp @ W.to(F64)).to(torch.float32).to(BF)), i
+    assert torch.equal(dbias.to(F64), sb)
+    assert torch.equal(dW, sW.to(torch.float32).to(BF))
+
+
+def test_recurrence_gate_gradient_past_2_31_elements():
+    # the last tokens, past 32-bit offsets, from the definition: the adjoint starts there
+    D, T, n, k = 4096, (1 << 19) + 70, 99, 110  # k: the roundings charged to a token in test_recur.py
+    cfg = ttt.make_recur_config(1, T, D)
+    draw = lambda seed, mean: torch.empty((T, D), device="cuda", dtype=BF).normal_(mean, 1, generator=rng(seed))
+    X, G = draw(1, 0), draw(2, 2)
+    H, dX, dG = torch.empty_like(X), torch.empty_like(X), torch.empty_like(X)
+    ttt.ttt_recur_fwd(cfg, X, G, None, None, H)
+    ttt.ttt_recur_bwd(cfg, X, G, None, None, H, X, None, dX, dG)
+    sync_ok()
+    carry = torch.zeros(D, dtype=F64, device="cuda")
+    err = torch.zeros_like(carry)
+    for t in range(T - 1, T - n, -1):
+        a, x, dh, prev = torch.sigmoid(G[t].to(F64)), X[t].to(F64), X[t].to(F64), H[t - 1].to(F64)
+        na, size = 1 - a, dh.abs() + carry.abs()
+        Dt, e = dh + carry, err + 2 * U32 * size
+        s = (prev - x) * a * na
+        assert_within("dX", dX[t], na * Dt, na * e + 50 * U32 * (na * Dt).abs())
+        assert_within("dG", dG[t], Dt * s, e * s.abs() + 100 * U32 * (Dt * s).abs())
+        err, carry = a * (e + k * U32 * size), a * Dt

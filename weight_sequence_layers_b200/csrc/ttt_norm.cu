@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(MAXT, 640 / MAXT)
   const int nsrc = dS ? 3 : 2;
   ring_init(bars, rg, smem, rg.stages * nsrc);
   int idx[NV];
-  slot_indices<RU == 2>(f, rg, idx);
+  slot_indices<NV <= 4>(f, rg, idx);
   Loader<E, VEC> ld(a, R, smem_u32(smem), smem_u32(bars.full));
   if (tid == 0) ld.issue(rg.stages, a, R, rg, X, dY, dS);
   float2 w[F::NP], dw[F::NP], db[F::NP];

@@ -12,9 +12,10 @@
 // Two kernels:
 //   pair: 256 x 256 tiles on CTA pairs (cta_group::2), persistent, two accumulators in TMEM so
 //         that the epilogue of one tile runs under the products of the next. Bound by the tensor
-//         cores: 16384 x 2048 x 2048 backward, both products 186 us = 1.48 PFLOP/s, and by power
-//         over longer times (32768 x 9728 x 2560 with SiLU and multiplier 1.14 ms alone, 1.37 ms
-//         back to back at 1.3 GHz; a plain library product of that size 1.21 ms there). Operands
+//         cores: 16384 x 2048 x 2048 backward, both products 187 us = 1.47 PFLOP/s, and by power
+//         over longer times (32768 x 9728 x 2560 with SiLU and multiplier 1.14 to 1.18 ms alone, 1.40
+//         to 1.45 ms back to back at 1.3 GHz, with P 1.25 and 1.52; the plain product 1.08 and 1.33,
+//         the library's 1.03 and 1.24). Operands
 //         of the epilogue by plain loads through shared memory were 2 % slower there and 20 % on
 //         small products.
 //   split: 128 x NT tiles with the roles of rows and columns exchanged (the weights' rows are the
@@ -908,7 +909,7 @@ cudaError_t run_pair(const Product* g, int n, int* counter, const Sums& sums, bo
 // The kernel of a product and the CTAs that share a tile's contraction (0: the pair kernel). The
 // choice hangs on the product alone, so that its sums come out the same in any call.
 // Split tiles as long as all of them are resident at a time, two an SM (543 x 3936 x 1696, 279
-// tiles: 23.4 us against the pair kernel's 25.5; 512 x 1024 x 1024: 15.4 against 20.5; beyond,
+// tiles: 23.4 us against the pair kernel's 25.5; 512 x 1024 x 1024: 14.3 against 20.5; beyond,
 // 200 rows' dW of 2560 x 2560: 27.6 against 21.3). With 32 rows or fewer always: the product is a
 // read of the weights. The backward's products stay with the pair kernel, which takes two in one
 // launch, unless they are deep (1024 x 2048 x 2048, both: 33.8 us against 44; 1024 x 1024 x 1024,

@@ -3,8 +3,8 @@
 //
 // A row is read once into registers, reduced twice there (the mean, then the centred squares: no
 // cancellation for rows with a large mean) and written once. Bound by HBM and, close behind, by the
-// instructions issued (16 and 22 for 32 values): 262144 x 128 bf16 forward 26 us = 5.1 TB/s,
-// 32768 x 2560 bf16 backward with dS 113 us = 5.9 TB/s and 9 us for the weight gradients' join
+// instructions issued (16 and 22 for 32 values): 262144 x 128 bf16 forward 28 us = 4.9 TB/s,
+// 32768 x 2560 bf16 backward with dS 113 us = 5.9 TB/s and 8 us for the weight gradients' join
 // (one CTA per row with the row read three times: 734 us and 5.8 ms).
 // A row belongs to a group of threads: 8 to 32 lanes of a warp for narrow rows (several rows
 // per CTA, sums by shuffles alone), the whole CTA for wide ones. CTA (h, s) walks a contiguous
@@ -908,10 +908,11 @@ Shape shape_of(const NormArgs& a, bool bwd) {
     if (n <= 256) { s.g = 32; s.nv = 8; return s; }
     if (n <= 512 && s.vec == 1 && !bwd) { s.g = 32; s.nv = 16; return s; }
     s.nv = n <= 2048 ? 4 : n <= 4096 ? 8 : n <= 8192 ? 16 : 32;
-    // (4 single elements with two rows per barrier where the runs are short: 4098 x 1021 float32
-    // 26.6 us against 28.7; 45288 x 1021 bf16 179 us against 155)
+    // 4 single elements with two rows per barrier against 8 with one: where runs are short or rows
+    // narrow the 4 (us, 4098 x 1263 float32 25.0 against 27.3, 6144 x 1021 31.2 against 31.4; 45288 x 601
+    // bf16 104 against 117), else the 8 (8800 x 1021 bf16 39.4 against 42.2, 45288 x 641 119 against 142)
     const bool long_runs = (long long)a.B * a.H * a.T >= 64 * kSMs;
-    if (bwd && (s.vec == 2 || n > 1280 || (n > 512 && long_runs))) s.nv = std::max(s.nv, 8);
+    if (bwd && (s.vec == 2 || n > 1280 || (n > 640 && long_runs))) s.nv = std::max(s.nv, 8);
   }
   s.g = 0;
   s.threads = ((n + s.nv - 1) / s.nv + 31) / 32 * 32;

@@ -15,7 +15,7 @@
 //
 // Bound by the time of a round (about 4,700 cycles: the gates' exponentials and reciprocals 1,500,
 // the join and its exchange 1,900, loads, outputs) before HBM: 32768 x 2560 bf16 forward 128 us =
-// 3.9 TB/s (one thread per feature: 19.8 ms), 8 x 2048 x 2048 backward 72 us = 5.6 TB/s. Measured
+// 3.9 TB/s (one thread per feature: 19.8 ms), 8 x 2048 x 2048 backward 73 us = 5.5 TB/s. Measured
 // and not kept: CTAs of 4 warps on 32 features (the same), three or four CTAs per SM with shorter
 // runs (192 us and more), joins by a releasing cluster barrier, which waits for the outputs'
 // stores too (371 us against 195 at the time).

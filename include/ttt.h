@@ -371,7 +371,8 @@ ttt_status ttt_norm_bwd(const ttt_norm_config* cfg, const void* S, const float* 
  *     h_t = a_t * h_{t-1} + u_t      (h_{-1} = h0; elementwise over D features)
  * TTT_GATE_DECAY:   G holds the decay itself (a = G, u = X), float32 as the layer's gamma.
  *     It may be above 1 in size: outputs are right as long as every state fits float32, whatever
- *     the products of the decays between them are.
+ *     the products of the decays between them are (a state that shrinks by more than 2^126 counts
+ *     as 0 from there on, even where later decays would make it grow again).
  * TTT_GATE_SIGMOID: G holds gate logits in dtype (a = sigmoid(G), u = (1 - a) X).
  * reset (nullable) marks the first token of every document of a packed sequence: at a token with
  * a nonzero byte the state before it counts as 0, whatever it held. */

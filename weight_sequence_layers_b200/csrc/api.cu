@@ -111,7 +111,6 @@ Path bwd_path(const LayerArgs& a, bool g_saved) {
   return PATH_NONE;
 }
 
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,

@@ -297,7 +297,7 @@ __device__ __forceinline__ bool within(float2 x, float most) { return within(x.x
 // WIDE: products may leave the range, where a run's A is above kSafe in size (marked beside its
 // reset). A product that did stays an infinity or NaN to the end of its lane's scan. In the scan of
 // the CTAs' maps, which all CTAs make alike, it sends the whole cluster the serial way; in the scan
-// of the runs, where the CTA's own map (lane 7's) is sound, this CTA;
+// of the runs, where the CTA's own map (lane 7's) is sound, this CTA alone.
 constexpr float kSafe = 3.9f;  // to the power of the 64 runs of a round: below 2^127
 template <int VC, bool WIDE, typename Through>
 __device__ __forceinline__ Vec<VC> join_runs(Joins<VC>& js, unsigned round, int cl, int rank,

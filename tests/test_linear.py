@@ -244,3 +244,11 @@ def test_many_tiles_in_place(both):
                                d[which])
             sync_ok()
             assert torch.equal(d[which], Y), which
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 12800, 1032), (16, 14208, 1032), (5, 6272, 2560), (24, 8960, 1032), (24, 9472, 1032),
+                                   (32, 4224, 2048), (100, 4096, 1024), (130, 3136, 2056), (64, 9088, 520),
+                                   (200, 1024, 4096), (77, 2112, 9728)])
+def test_contractions_shared_up_to_what_is_resident(M, N, K):
+    # tiles on both sides of the CTAs that fit, shared 1, 2, 4 and 8 ways, with ragged edges
+    check_forward(case(M, N, K, "silu", bias=True, mul=True, residual=True, seed=N))
